@@ -184,7 +184,7 @@ def _quantize(k, v, bits):
 
     def group(x, dim):  # the group's axis is `dim`
         lo, hi = x.amin(dim, keepdim=True), x.amax(dim, keepdim=True)
-        s = (hi - lo) / top
+        s = (hi - lo) / torch.full_like(lo, top)  # a quotient; by a Python number torch multiplies by its reciprocal
         code = torch.where(s == 0, torch.zeros_like(x), torch.round((x - lo) / s).clamp(0, top))
         return code, s, lo
 
