@@ -108,6 +108,12 @@ extern "C" {
 #define S4KV_BLOCK_BYTES_INT8 4864 /* 8-bit codes */
 #define S4KV_BLOCK_BYTES_INT2 1792 /* 2-bit codes */
 #define S4KV_MAX_GQA_GROUP 8
+#define S4KV_MAX_TREE_NODES 64
+
+/* element types of a row of probabilities */
+#define S4KV_PROB_F32 0
+#define S4KV_PROB_F16 1
+#define S4KV_PROB_BF16 2
 
 /* status codes returned by every call */
 #define S4KV_OK 0
@@ -122,6 +128,8 @@ extern "C" {
 #define S4KV_EFLAG_SLOT 2u       /* slot_mapping != block_tables[b][pos/16]*16 + pos%16 */
 #define S4KV_EFLAG_SEQ_LEN 4u    /* seq_lens / cu_new inconsistent with the call */
 #define S4KV_EFLAG_TIMEOUT 8u    /* a bounded pipeline wait gave up */
+#define S4KV_EFLAG_TREE 16u      /* cu_nodes, parents, tokens or a path inconsistent with the call */
+#define S4KV_EFLAG_PROBS 32u     /* a row of probabilities without a finite positive sum */
 
 /* Caller-owned description of one layer's cache.  Plain data; the library
  * never frees or retains it. */
@@ -389,6 +397,119 @@ S4KV_API int s4kv_swap_out(const s4kv_cache_t *cache, const int32_t *pages, int 
  * caller points the sequence's page table at them). */
 S4KV_API int s4kv_swap_in(const s4kv_cache_t *cache, const int32_t *pages, int n,
                           void *staging, const void *host_src, void *stream);
+
+/* ---- speculative decoding ("KV-Cache-Optimierung -- PagedAttention,
+ * quantisierter KV, Speculative Cache", "Kernpunkte"): a draft proposes a tree
+ * of tokens a sequence, one pass of the target attends over the cache for all
+ * of them (s4kv_tree_attention), the target's probabilities accept a path
+ * (s4kv_verify_tree), and that path's keys and values enter the cache
+ * (s4kv_append_path).  Lengths and paths stay on the device, so a step needs
+ * no synchronisation with the host and can be captured into a graph.
+ *
+ * Trees: sequence b owns the nodes cu_nodes[b] .. cu_nodes[b+1]-1 of packed
+ * arrays, at most S4KV_MAX_TREE_NODES of them; a node is named by its index
+ * inside its sequence.  parents[node] is the index of its parent, which is
+ * lower than its own, or -1 (a child of the sequence's last cached token).
+ * A sequence may own no node. */
+
+/* Bytes of device workspace s4kv_tree_attention needs on the CURRENT device
+ * for these bounds.  Zero-fill it once after allocation; every completed call
+ * leaves its counters at zero again, and a workspace sized for some bounds
+ * serves smaller ones.  After a call that set S4KV_EFLAG_TIMEOUT zero-fill it
+ * again.  S4KV_ERR_UNSUPPORTED where s4kv_check_model refuses the heads or
+ * max_nodes_per_seq exceeds S4KV_MAX_TREE_NODES; needs a CUDA device. */
+S4KV_API int s4kv_tree_workspace_size(int num_q_heads, int num_kv_heads, int batch,
+                                      int max_nodes_per_seq, size_t *bytes);
+
+/* Attention of every drafted token over its sequence's cache, its ancestors
+ * in the tree and itself.  The drafted tokens are not in the cache, and
+ * nothing is written to it.
+ *  q       device fp16 [n_nodes][num_q_heads][128], 16-B aligned; query head
+ *          j reads kv head j / (num_q_heads / num_kv_heads).
+ *  k, v    device fp16 [n_nodes][num_kv_heads][128], 16-B aligned: the
+ *          drafted tokens' own keys and values (rotated for their positions,
+ *          as for s4kv_append).
+ *  cu_nodes  device int32 [batch+1], cu_nodes[0] = 0, nondecreasing,
+ *          cu_nodes[batch] <= n_nodes.
+ *  parents device int32 [n_nodes].  A parent outside [-1, own index) sets
+ *          S4KV_EFLAG_TREE and counts as -1.
+ *  seq_lens, block_tables  as for s4kv_decode_attention: the cached tokens,
+ *          without the drafted ones; 0 is allowed.
+ *  max_nodes_per_seq  host bound on any sequence's node count, at most
+ *          S4KV_MAX_TREE_NODES.  A sequence with more nodes, or bad cu_nodes
+ *          (S4KV_EFLAG_TREE) or a bad length (S4KV_EFLAG_SEQ_LEN), is skipped.
+ *  out     device fp16 [n_nodes][num_q_heads][128], 16-B aligned; rows of no
+ *          sequence and rows of skipped sequences are left untouched.
+ *  workspace  device, >= s4kv_tree_workspace_size bytes, 16-B aligned.
+ * Any code width of the cache.  Calls sharing one workspace must not overlap
+ * on the device. */
+S4KV_API int s4kv_tree_attention(const s4kv_cache_t *cache, const void *q, const void *k,
+                                 const void *v, int num_q_heads, int n_nodes,
+                                 const int32_t *cu_nodes, const int32_t *parents,
+                                 const int32_t *seq_lens, const int32_t *block_tables,
+                                 int batch, int max_pages_per_seq, int max_nodes_per_seq,
+                                 float sm_scale, void *out, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* Accept drafted tokens against the target's probabilities, from given random
+ * numbers: the accepted tokens and the one that follows them are distributed
+ * as the target alone would have drawn them.
+ * Node 0 of a sequence is its last token, known already and accepted; the
+ * children of node i are the tokens proposed to follow it.  With cur = node 0,
+ * R = target row of cur and M = 1, the children of cur are tried in index
+ * order: child c, token x, is accepted when
+ *     uniforms[c] * M * Q(x) < R(x),
+ * Q = draft row of cur (the children of a node are independent draws from that
+ * one row), or 1 when draft_probs is NULL (proposals chosen without
+ * randomness, e.g. the draft's best tokens).  An accepted child becomes cur.
+ * A rejected one changes what is left: R <- max(R - M Q, 0) elementwise and
+ * M <- sum of R (draft row), or R(x) <- 0 and M <- M - R(x) (no draft row).  When no
+ * child is left, next_token = the lowest v with R(0) + .. + R(v) >
+ * uniforms[node 0] * sum of R.  If nothing is left of R, R is cur's target row
+ * again.  Entries that are negative or NaN count as 0.  All of it is
+ * computed in 64 bits.
+ *  tokens, parents  device int32 [n_nodes]; cu_nodes device int32 [batch+1].
+ *          A token outside [0, vocab) sets S4KV_EFLAG_TREE and is passed over;
+ *          a node with a parent outside [0, own index) is no node's child.
+ *  target_probs  device [n_nodes] rows of vocab entries, row i at element
+ *          i * target_stride: what the target gives to follow node i, summing
+ *          to 1.  draft_probs the same for the draft, or NULL.
+ *  prob_type  S4KV_PROB_F32, _F16 or _BF16, of both; rows aligned to their
+ *          element.
+ *  uniforms  device fp32 [n_nodes], in [0, 1).
+ *  path    device int32 [batch][max_nodes_per_seq]: the accepted nodes from
+ *          node 0 on, then -1.
+ *  path_len, next_token  device int32 [batch].  A sequence without nodes, or
+ *          with bad cu_nodes (S4KV_EFLAG_TREE), gets 0 and -1; next_token is -1
+ *          too, with S4KV_EFLAG_PROBS, where no target row has a finite
+ *          positive sum.
+ *  err_flag  device word as in s4kv_cache_t, or NULL. */
+S4KV_API int s4kv_verify_tree(const int32_t *tokens, const int32_t *parents,
+                              const int32_t *cu_nodes, int n_nodes, int batch,
+                              int max_nodes_per_seq, const void *target_probs,
+                              int64_t target_stride, const void *draft_probs,
+                              int64_t draft_stride, int prob_type, int vocab,
+                              const float *uniforms, int32_t *path, int32_t *path_len,
+                              int32_t *next_token, uint32_t *err_flag, void *stream);
+
+/* s4kv_append of the accepted path of every sequence: its tokens
+ * path[b][0 .. path_len[b]-1] (node indices) take the positions seq_lens[b]
+ * onwards; pages that they complete are quantized, byte for byte as s4kv_append
+ * of the same rows does.
+ *  k, v    device fp16 [n_nodes][num_kv_heads][128], 16-B aligned: the nodes'
+ *          keys and values, as given to s4kv_tree_attention.
+ *  path    device int32 [batch][max_nodes_per_seq]; path_len device int32
+ *          [batch]: as s4kv_verify_tree writes them.  0 appends nothing.
+ *  seq_lens  device int32 [batch]: lengths BEFORE the append.
+ *  new_lens  device int32 [batch], no part of seq_lens: lengths after it.
+ * A sequence with bad cu_nodes or path (S4KV_EFLAG_TREE), or without room in
+ * its page table (S4KV_EFLAG_SEQ_LEN), is skipped whole: its new length is its
+ * old one. */
+S4KV_API int s4kv_append_path(const s4kv_cache_t *cache, const void *k, const void *v,
+                              int n_nodes, const int32_t *cu_nodes, const int32_t *path,
+                              const int32_t *path_len, int max_nodes_per_seq,
+                              const int32_t *seq_lens, const int32_t *block_tables, int batch,
+                              int max_pages_per_seq, int32_t *new_lens, void *stream);
 
 /* Synchronize `stream`, read the cache's err_flag into *flags and clear it
  * when `clear` != 0.  Returns S4KV_ERR_DEVICE_CHECK when bits were set. */

@@ -21,10 +21,11 @@ BLOCK_BYTES = 2816
 BLOCK_BYTES_INT8 = 4864
 BLOCK_BYTES_INT2 = 1792
 MAX_GQA_GROUP = 8
+MAX_TREE_NODES = 64
 NOALLOC_SCRATCH_BYTES = 24 * 1024 * 1024
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE_CHECK, ERR_WORKSPACE = range(6)
-EFLAG_PAGE_RANGE, EFLAG_SLOT, EFLAG_SEQ_LEN, EFLAG_TIMEOUT = 1, 2, 4, 8
+EFLAG_PAGE_RANGE, EFLAG_SLOT, EFLAG_SEQ_LEN, EFLAG_TIMEOUT, EFLAG_TREE, EFLAG_PROBS = 1, 2, 4, 8, 16, 32
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libs4kv.so")
@@ -36,7 +37,7 @@ class s4kv_cache_t(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("bits", ctypes.c_int32)]
 
 
-_P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _SZ, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 _CP = ctypes.POINTER(s4kv_cache_t)
 _SIGS = {
     "s4kv_version": ([], _I),
@@ -60,6 +61,10 @@ _SIGS = {
     "s4kv_fork_residual": ([_CP, _P, _P, _I, _P], _I),
     "s4kv_swap_out": ([_CP, _P, _I, _P, _P, _P], _I),
     "s4kv_swap_in": ([_CP, _P, _I, _P, _P, _P], _I),
+    "s4kv_tree_workspace_size": ([_I, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
+    "s4kv_tree_attention": ([_CP, _P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, ctypes.c_float, _P, _P, _SZ, _P], _I),
+    "s4kv_verify_tree": ([_P, _P, _P, _I, _I, _I, _P, _L, _P, _L, _I, _I, _P, _P, _P, _P, _P, _P], _I),
+    "s4kv_append_path": ([_CP, _P, _P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _P, _P], _I),
     "s4kv_get_error": ([_CP, ctypes.POINTER(ctypes.c_uint32), _I, _P], _I),
 }
 EXPORTED = tuple(_SIGS)
@@ -335,6 +340,149 @@ def s4kv_swap_in(cache: S4KVCache, pages, staging, host_src, stream=None):
                            _ptr(staging, torch.uint8, "staging"), ctypes.c_void_p(host_src.data_ptr()),
                            _stream(stream))
     _check(st, "s4kv_swap_in")
+
+
+# ---- speculative decoding: attention of a drafted tree, its verification and
+# the append of the accepted path.  These calls run on their tensors' device
+# (all on one), whichever device is current, and by default on that device's
+# current stream.
+
+def _device(lead, *tensors):
+    """The one CUDA device of all these tensors."""
+    dev = lead.device
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got {t.device}")
+    return dev
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _call(dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` current."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(stream))
+
+
+def s4kv_tree_workspace_size(num_q_heads: int, num_kv_heads: int, batch: int, max_nodes_per_seq: int) -> int:
+    n = _SZ(0)
+    _check(lib().s4kv_tree_workspace_size(num_q_heads, num_kv_heads, batch, max_nodes_per_seq, ctypes.byref(n)),
+           "s4kv_tree_workspace_size")
+    return n.value
+
+
+def tree_workspace(num_q_heads: int, num_kv_heads: int, batch: int, max_nodes_per_seq: int, device="cuda"):
+    """Zero-filled workspace of the size s4kv_tree_attention needs."""
+    import torch
+    with torch.cuda.device(device):
+        n = s4kv_tree_workspace_size(num_q_heads, num_kv_heads, batch, max_nodes_per_seq)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def s4kv_tree_attention(cache: S4KVCache, q, k, v, cu_nodes, parents, seq_lens, block_tables, out,
+                        max_nodes_per_seq: int, workspace, sm_scale: float | None = None, stream=None):
+    """Attention of drafted tokens (q fp16 [n_nodes][num_q_heads][128]; their
+    keys and values k, v fp16 [n_nodes][kv_heads][128], not in the cache) over
+    the cached tokens, their ancestors in the tree and themselves.  Sequence b
+    owns the nodes cu_nodes[b] .. cu_nodes[b+1]-1; parents int32 [n_nodes] are
+    indices inside the sequence, -1 for a child of the last cached token."""
+    import torch
+    if sm_scale is None:
+        sm_scale = HEAD_DIM ** -0.5
+    n_nodes, num_q_heads, _ = q.shape
+    batch, max_pages = block_tables.shape
+    kv = (n_nodes, cache.num_kv_heads, HEAD_DIM)
+    _shape(q, (n_nodes, num_q_heads, HEAD_DIM), "q")
+    _shape(k, kv, "k")
+    _shape(v, kv, "v")
+    _shape(out, tuple(q.shape), "out")
+    _shape(cu_nodes, (batch + 1,), "cu_nodes")
+    _shape(parents, (n_nodes,), "parents")
+    _shape(seq_lens, (batch,), "seq_lens")
+    dev = _device(cache.pool, q, k, v, out, cu_nodes, parents, seq_lens, block_tables, workspace)
+    f16, i32 = torch.float16, torch.int32
+    _check(_call(dev, stream, lib().s4kv_tree_attention, cache.ref, _ptr(q, f16, "q"), _ptr(k, f16, "k"),
+                 _ptr(v, f16, "v"), num_q_heads, n_nodes, _ptr(cu_nodes, i32, "cu_nodes"),
+                 _ptr(parents, i32, "parents"), _ptr(seq_lens, i32, "seq_lens"),
+                 _ptr(block_tables, i32, "block_tables"), batch, max_pages, int(max_nodes_per_seq), float(sm_scale),
+                 _ptr(out, f16, "out"), _ptr(workspace, torch.uint8, "workspace"), workspace.numel()),
+           "s4kv_tree_attention")
+
+
+def s4kv_verify_tree(tokens, parents, cu_nodes, target_probs, draft_probs, uniforms, path, path_len, next_token,
+                     err_flag=None, stream=None):
+    """Accept a path of every sequence's tree against the target's
+    probabilities (target_probs [n_nodes][vocab], fp32, fp16 or bf16; row i is
+    what follows node i; rows may be strided), with uniforms fp32 [n_nodes] in
+    [0, 1).  draft_probs: the rows from which each node's children were drawn,
+    or None for proposals chosen without randomness.  Fills path int32
+    [batch][max_nodes], path_len and next_token int32 [batch]."""
+    import torch
+    types = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    n_nodes, vocab = target_probs.shape
+    batch, max_nodes = path.shape
+    for name, rows in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+        if rows is None:
+            continue
+        if rows.dtype not in types or rows.dtype != target_probs.dtype:
+            raise TypeError(f"{name}: expected float32, float16 or bfloat16 (one type), got {rows.dtype}")
+        _shape(rows, (n_nodes, vocab), name)
+        if rows.numel() and rows.stride(1) != 1 and vocab > 1:
+            raise ValueError(f"{name}: the entries of a row must be contiguous")
+    for name, t, shape in (("tokens", tokens, (n_nodes,)), ("parents", parents, (n_nodes,)),
+                           ("cu_nodes", cu_nodes, (batch + 1,)), ("uniforms", uniforms, (n_nodes,)),
+                           ("path_len", path_len, (batch,)), ("next_token", next_token, (batch,))):
+        _shape(t, shape, name)
+    dev = _device(target_probs, draft_probs, tokens, parents, cu_nodes, uniforms, path, path_len, next_token, err_flag)
+    i32 = torch.int32
+
+    def rows_of(t):  # address and stride; one row has no stride of its own
+        if t is None:
+            return None, 0
+        return ctypes.c_void_p(t.data_ptr()), t.stride(0) if n_nodes > 1 else vocab
+
+    tp, ts = rows_of(target_probs)
+    dp, ds = rows_of(draft_probs)
+    _check(_call(dev, stream, lib().s4kv_verify_tree, _ptr(tokens, i32, "tokens"), _ptr(parents, i32, "parents"),
+                 _ptr(cu_nodes, i32, "cu_nodes"), n_nodes, batch, max_nodes, tp, ts, dp, ds, types[target_probs.dtype],
+                 vocab, _ptr(uniforms, torch.float32, "uniforms"), _ptr(path, i32, "path"),
+                 _ptr(path_len, i32, "path_len"), _ptr(next_token, i32, "next_token"),
+                 _ptr(err_flag, i32, "err_flag")), "s4kv_verify_tree")
+
+
+def s4kv_append_path(cache: S4KVCache, k, v, cu_nodes, path, path_len, seq_lens, block_tables, new_lens, stream=None):
+    """Append the accepted path of every sequence (path int32
+    [batch][max_nodes], path_len int32 [batch], as s4kv_verify_tree fills them)
+    to the cache: rows of the nodes' k, v fp16 [n_nodes][kv_heads][128] at the
+    positions seq_lens[b] onwards (lengths BEFORE the append).  Fills new_lens
+    int32 [batch], a tensor of its own."""
+    import torch
+    n_nodes = k.shape[0]
+    batch, max_pages = block_tables.shape
+    kv = (n_nodes, cache.num_kv_heads, HEAD_DIM)
+    _shape(k, kv, "k")
+    _shape(v, kv, "v")
+    _shape(cu_nodes, (batch + 1,), "cu_nodes")
+    _shape(path, (batch, path.shape[-1]), "path")
+    _shape(path_len, (batch,), "path_len")
+    _shape(seq_lens, (batch,), "seq_lens")
+    _shape(new_lens, (batch,), "new_lens")
+    dev = _device(cache.pool, k, v, cu_nodes, path, path_len, seq_lens, block_tables, new_lens)
+    f16, i32 = torch.float16, torch.int32
+    _check(_call(dev, stream, lib().s4kv_append_path, cache.ref, _ptr(k, f16, "k"), _ptr(v, f16, "v"), n_nodes,
+                 _ptr(cu_nodes, i32, "cu_nodes"), _ptr(path, i32, "path"), _ptr(path_len, i32, "path_len"),
+                 path.shape[1], _ptr(seq_lens, i32, "seq_lens"), _ptr(block_tables, i32, "block_tables"), batch,
+                 max_pages, _ptr(new_lens, i32, "new_lens")), "s4kv_append_path")
 
 
 def s4kv_get_error(cache: S4KVCache, clear: bool = True, stream=None) -> int:

@@ -335,6 +335,190 @@ int s4kv_prefill_attention(const s4kv_cache_t *cache, const void *q, int num_q_h
   return S4KV_OK;
 }
 
+namespace {
+
+// Workspace of the tree attention: [ml][partial outputs][tickets].  The first
+// two depend on the device alone, so that a workspace sized for some bounds
+// serves smaller ones.
+struct TreeWs {
+  size_t part, tickets, total;
+};
+
+int tree_ws_layout(int num_q_heads, int num_kv_heads, int batch, int max_nodes, TreeWs *w, int *ctas) {
+  const int rc = s4kv_check_model(S4KV_HEAD_DIM, S4KV_PAGE_TOKENS, num_q_heads, num_kv_heads);
+  if (rc != S4KV_OK) return rc;
+  if (batch < 0 || max_nodes <= 0) return S4KV_ERR_INVALID_ARG;
+  if (max_nodes > S4KV_MAX_TREE_NODES) return S4KV_ERR_UNSUPPORTED;
+  const int blocks = (max_nodes * (num_q_heads / num_kv_heads) + kTreeRows - 1) / kTreeRows;
+  const unsigned long long units = static_cast<unsigned long long>(batch) * num_kv_heads * blocks;
+  if (units > 0x7FFFFFFFull) return S4KV_ERR_INVALID_ARG;
+  DeviceShape d;
+  const int rd = device_shape(&d);
+  if (rd != S4KV_OK) return rd;
+  const size_t slots = static_cast<size_t>(2) * d.num_sms * kTreeRows;
+  w->part = (slots * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
+  w->tickets = w->part + slots * S4KV_HEAD_DIM * sizeof(float);
+  w->total = w->tickets + static_cast<size_t>(units) * 2 * sizeof(uint32_t);
+  *ctas = d.num_sms;
+  return S4KV_OK;
+}
+
+}  // namespace
+
+int s4kv_tree_workspace_size(int num_q_heads, int num_kv_heads, int batch, int max_nodes_per_seq, size_t *bytes) {
+  if (bytes == nullptr) return S4KV_ERR_INVALID_ARG;
+  TreeWs w;
+  int ctas = 0;
+  const int rc = tree_ws_layout(num_q_heads, num_kv_heads, batch, max_nodes_per_seq, &w, &ctas);
+  if (rc == S4KV_OK) *bytes = w.total;
+  return rc;
+}
+
+int s4kv_tree_attention(const s4kv_cache_t *cache, const void *q, const void *k, const void *v, int num_q_heads,
+                        int n_nodes, const int32_t *cu_nodes, const int32_t *parents, const int32_t *seq_lens,
+                        const int32_t *block_tables, int batch, int max_pages_per_seq, int max_nodes_per_seq,
+                        float sm_scale, void *out, void *workspace, size_t workspace_bytes, void *stream) {
+  int rc = check_cache(cache);
+  if (rc != S4KV_OK) return rc;
+  rc = s4kv_check_model(cache->head_dim, cache->page_tokens, num_q_heads, cache->num_kv_heads);
+  if (rc != S4KV_OK) return rc;
+  if (n_nodes < 0 || batch < 0 || batch > cache->max_seqs || max_pages_per_seq <= 0 || max_nodes_per_seq <= 0 ||
+      max_pages_per_seq > 0x7FFFFFFF / S4KV_PAGE_TOKENS)
+    return S4KV_ERR_INVALID_ARG;
+  if (max_nodes_per_seq > S4KV_MAX_TREE_NODES) return S4KV_ERR_UNSUPPORTED;
+  if (!(std::isfinite(sm_scale)) || sm_scale <= 0.0f) return S4KV_ERR_INVALID_ARG;
+  if (n_nodes == 0 || batch == 0) return S4KV_OK;
+  if (!q || !k || !v || !cu_nodes || !parents || !seq_lens || !block_tables || !out) return S4KV_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_nodes, 4) ||
+      !aligned(parents, 4) || !aligned(seq_lens, 4) || !aligned(block_tables, 4))
+    return S4KV_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 16)) return S4KV_ERR_WORKSPACE;
+  TreeWs w;
+  int ctas = 0;
+  rc = tree_ws_layout(num_q_heads, cache->num_kv_heads, batch, max_nodes_per_seq, &w, &ctas);
+  if (rc != S4KV_OK) return rc;
+  if (workspace_bytes < w.total) return S4KV_ERR_WORKSPACE;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  TreeParams p;
+  p.pool = static_cast<const uint8_t *>(cache->pool);
+  p.res_k = static_cast<const __half *>(cache->res_k);
+  p.res_v = static_cast<const __half *>(cache->res_v);
+  p.q = static_cast<const __half *>(q);
+  p.k = static_cast<const __half *>(k);
+  p.v = static_cast<const __half *>(v);
+  p.out = static_cast<__half *>(out);
+  p.cu_nodes = cu_nodes;
+  p.parents = parents;
+  p.seq_lens = seq_lens;
+  p.block_tables = block_tables;
+  p.part_ml = reinterpret_cast<float2 *>(ws);
+  p.part = reinterpret_cast<float *>(ws + w.part);
+  p.tickets = reinterpret_cast<uint32_t *>(ws + w.tickets);
+  p.err = cache->err_flag;
+  p.batch = batch;
+  p.n_nodes = n_nodes;
+  p.max_nodes = max_nodes_per_seq;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.group = num_q_heads / cache->num_kv_heads;
+  p.max_pages = max_pages_per_seq;
+  p.num_pages = cache->num_pages;
+  p.scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
+  p.bits = cache_bits(cache);
+  p.num_ctas = ctas;
+  if (launch_tree(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return S4KV_ERR_CUDA;
+  }
+  return S4KV_OK;
+}
+
+int s4kv_verify_tree(const int32_t *tokens, const int32_t *parents, const int32_t *cu_nodes, int n_nodes, int batch,
+                     int max_nodes_per_seq, const void *target_probs, int64_t target_stride, const void *draft_probs,
+                     int64_t draft_stride, int prob_type, int vocab, const float *uniforms, int32_t *path,
+                     int32_t *path_len, int32_t *next_token, uint32_t *err_flag, void *stream) {
+  if (n_nodes < 0 || batch < 0 || max_nodes_per_seq <= 0 || vocab <= 0) return S4KV_ERR_INVALID_ARG;
+  if (max_nodes_per_seq > S4KV_MAX_TREE_NODES) return S4KV_ERR_UNSUPPORTED;
+  if (prob_type != S4KV_PROB_F32 && prob_type != S4KV_PROB_F16 && prob_type != S4KV_PROB_BF16)
+    return S4KV_ERR_INVALID_ARG;
+  if (target_stride < vocab || (draft_probs && draft_stride < vocab)) return S4KV_ERR_INVALID_ARG;
+  if (batch == 0) return S4KV_OK;
+  if (!cu_nodes || !path || !path_len || !next_token) return S4KV_ERR_INVALID_ARG;
+  if (n_nodes > 0 && (!tokens || !parents || !target_probs || !uniforms)) return S4KV_ERR_INVALID_ARG;
+  const size_t es = prob_type == S4KV_PROB_F32 ? 4 : 2;
+  if (!aligned(tokens, 4) || !aligned(parents, 4) || !aligned(cu_nodes, 4) || !aligned(uniforms, 4) ||
+      !aligned(path, 4) || !aligned(path_len, 4) || !aligned(next_token, 4) || !aligned(err_flag, 4) ||
+      !aligned(target_probs, es) || !aligned(draft_probs, es))
+    return S4KV_ERR_INVALID_ARG;
+  VerifyParams p;
+  p.tokens = tokens;
+  p.parents = parents;
+  p.cu_nodes = cu_nodes;
+  p.target = target_probs;
+  p.draft = draft_probs;
+  p.uniforms = uniforms;
+  p.path = path;
+  p.path_len = path_len;
+  p.next_token = next_token;
+  p.err = err_flag;
+  p.target_stride = target_stride;
+  p.draft_stride = draft_stride;
+  p.prob_type = prob_type;
+  p.vocab = vocab;
+  p.n_nodes = n_nodes;
+  p.batch = batch;
+  p.max_nodes = max_nodes_per_seq;
+  if (launch_verify(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return S4KV_ERR_CUDA;
+  }
+  return S4KV_OK;
+}
+
+int s4kv_append_path(const s4kv_cache_t *cache, const void *k, const void *v, int n_nodes, const int32_t *cu_nodes,
+                     const int32_t *path, const int32_t *path_len, int max_nodes_per_seq, const int32_t *seq_lens,
+                     const int32_t *block_tables, int batch, int max_pages_per_seq, int32_t *new_lens, void *stream) {
+  const int rc = check_cache(cache);
+  if (rc != S4KV_OK) return rc;
+  if (n_nodes < 0 || batch < 0 || batch > cache->max_seqs || max_pages_per_seq <= 0 || max_nodes_per_seq <= 0 ||
+      max_pages_per_seq > 0x7FFFFFFF / S4KV_PAGE_TOKENS)
+    return S4KV_ERR_INVALID_ARG;
+  if (max_nodes_per_seq > S4KV_MAX_TREE_NODES) return S4KV_ERR_UNSUPPORTED;
+  if (batch == 0) return S4KV_OK;
+  if (batch > 65535 || cache->num_kv_heads > 65535) return S4KV_ERR_INVALID_ARG;
+  if (!cu_nodes || !path || !path_len || !seq_lens || !block_tables || !new_lens) return S4KV_ERR_INVALID_ARG;
+  if (n_nodes > 0 && (!k || !v)) return S4KV_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_nodes, 4) || !aligned(path, 4) || !aligned(path_len, 4) ||
+      !aligned(seq_lens, 4) || !aligned(block_tables, 4) || !aligned(new_lens, 4))
+    return S4KV_ERR_INVALID_ARG;
+  // other CTAs of a sequence read its old length while one writes the new one
+  if (new_lens < seq_lens + batch && seq_lens < new_lens + batch) return S4KV_ERR_INVALID_ARG;
+  PathParams p;
+  p.pool = static_cast<uint8_t *>(cache->pool);
+  p.res_k = static_cast<__half *>(cache->res_k);
+  p.res_v = static_cast<__half *>(cache->res_v);
+  p.err = cache->err_flag;
+  p.k = static_cast<const __half *>(k);
+  p.v = static_cast<const __half *>(v);
+  p.cu_nodes = cu_nodes;
+  p.path = path;
+  p.path_len = path_len;
+  p.seq_lens = seq_lens;
+  p.block_tables = block_tables;
+  p.new_lens = new_lens;
+  p.num_pages = cache->num_pages;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.max_pages = max_pages_per_seq;
+  p.max_nodes = max_nodes_per_seq;
+  p.n_nodes = n_nodes;
+  p.bits = cache_bits(cache);
+  if (launch_append_path(p, batch, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return S4KV_ERR_CUDA;
+  }
+  return S4KV_OK;
+}
+
 int s4kv_dequant_page(const s4kv_cache_t *cache, int physical_page, void *out_k, void *out_v,
                       int out_fp32, void *stream) {
   int rc = check_cache(cache);

@@ -87,6 +87,87 @@ struct FusedAppend {
   const __half *v_new;
 };
 
+// Attention of a tree of drafted tokens over the cache (s4kv_tree_attention).
+struct TreeParams {
+  const uint8_t *pool;
+  const __half *res_k;
+  const __half *res_v;
+  const __half *q;  // [n_nodes][num_q_heads][128]
+  const __half *k;  // [n_nodes][num_kv_heads][128]
+  const __half *v;
+  __half *out;
+  const int32_t *cu_nodes;
+  const int32_t *parents;
+  const int32_t *seq_lens;
+  const int32_t *block_tables;
+  float2 *part_ml;    // [2 * num_ctas][64] (reference, sum of weights) of a piece's rows
+  float *part;        // [2 * num_ctas][64][128] its unnormalised output
+  uint32_t *tickets;  // [batch * num_kv_heads * row blocks][2], zero between calls
+  uint32_t *err;
+  int batch;
+  int n_nodes;
+  int max_nodes;
+  int num_q_heads;
+  int num_kv_heads;
+  int group;
+  int max_pages;
+  int num_pages;
+  float scale_log2;  // sm_scale * log2(e)
+  int bits;
+  int num_ctas;
+};
+
+// Query rows (node, head of the group) that one unit of the tree attention
+// holds.
+constexpr int kTreeRows = 64;
+
+// Verification of drafted tokens (s4kv_verify_tree).
+struct VerifyParams {
+  const int32_t *tokens;
+  const int32_t *parents;
+  const int32_t *cu_nodes;
+  const void *target;
+  const void *draft;  // nullptr: the proposals are point masses
+  const float *uniforms;
+  int32_t *path;
+  int32_t *path_len;
+  int32_t *next_token;
+  uint32_t *err;
+  long long target_stride;  // elements
+  long long draft_stride;
+  int prob_type;
+  int vocab;
+  int n_nodes;
+  int batch;
+  int max_nodes;
+};
+
+// Append of accepted paths (s4kv_append_path).
+struct PathParams {
+  uint8_t *pool;
+  __half *res_k;
+  __half *res_v;
+  uint32_t *err;
+  const __half *k;
+  const __half *v;
+  const int32_t *cu_nodes;
+  const int32_t *path;
+  const int32_t *path_len;
+  const int32_t *seq_lens;
+  const int32_t *block_tables;
+  int32_t *new_lens;
+  int num_pages;
+  int num_kv_heads;
+  int max_pages;
+  int max_nodes;
+  int n_nodes;
+  int bits;
+};
+
+cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream);
+cudaError_t launch_append_path(const PathParams &p, int batch, cudaStream_t stream);
+
 void launch_append(const AppendParams &p, int batch, int max_new, cudaStream_t stream);
 void launch_dequant(const DequantParams &p, cudaStream_t stream);
 void launch_move(const MoveParams &p, cudaStream_t stream);
