@@ -93,7 +93,6 @@ constexpr float kSlack = 8.0f;                   // log2 slack of the softmax re
 #define S4KV_PREFILL_POLY_OF8 3
 #endif
 constexpr int kPolyOf8 = S4KV_PREFILL_POLY_OF8;  // eighths of the exponentials on the FMA pipe
-constexpr long long kWaitLimit = 2000000000LL;   // about one second
 // S: M = 128, N = 128 keys (Q against K_hi, fp16 K = 16 per MMA, then Q8
 // against K_lo, e5m2 K = 32 per MMA, accumulated); PV: M = 128, N = 128
 constexpr uint32_t kIdescS = tc05::idesc_f16_f32(128, kKeyTile);
@@ -130,24 +129,6 @@ constexpr uint32_t op_smem_bytes() {
   return kHalfTileBytes + kOpPages * Fmt<kBits>::kBlock + 1024;
 }
 
-// Bounded wait for a barrier phase; gives up after about a second or as soon
-// as another role has raised the CTA's abort flag.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const volatile int *abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort || clock64() - t0 > kWaitLimit) return false;
-  }
-}
-
-// Bounded wait used while draining copies before the CTA exits (time only).
-__device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity) && clock64() - t0 <= kWaitLimit) {
-  }
-}
-
 // 2^x for a pair, on the FMA/ALU pipes instead of the MUFU pipe.  Cody and
 // Waite's range reduction: x = j + f with j = rint(x) (adding 1.5 * 2^23
 // rounds x to an integer held in the sum's low mantissa bits) and
@@ -171,51 +152,6 @@ __device__ __forceinline__ float2 exp2_poly2(float2 x) {
                      __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
 }
 
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
-}
-__device__ __forceinline__ void sts16(uint32_t addr, uint16_t a) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(a) : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ uint4 lds128_at(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32_at(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64_at(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
-
-// max of three floats in one instruction (sm_100); a NaN operand is ignored
-// as by fmaxf
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t hfma2_u32(uint32_t a, uint32_t b, uint32_t c) {
-  return h2_as_u32(__hfma2(u32_as_h2(a), u32_as_h2(b), u32_as_h2(c)));
-}
-
 // Two fp32 values rounded to e5m2 (round to nearest even, saturating), the
 // first in the low byte.
 __device__ __forceinline__ uint16_t e5m2x2(float first, float second) {
@@ -223,14 +159,6 @@ __device__ __forceinline__ uint16_t e5m2x2(float first, float second) {
   asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(d) : "f"(second), "f"(first));
   return d;
 }
-// Two fp16 values (a pair in one word, the lower element in the low half)
-// rounded to e5m2, the lower element in the low byte.
-__device__ __forceinline__ uint16_t e5m2x2_of_f16x2(uint32_t x) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(d) : "r"(x));
-  return d;
-}
-
 // Two keys (fp16 codes in `codes`) dequantized in fp32 (code * scale + zero:
 // the product is exact, so one rounding) and split into an fp16 hi part and
 // the e5m2 rounding of the remainder (lo, the lower key in the low byte).
@@ -241,12 +169,6 @@ __device__ __forceinline__ void split_key(uint32_t codes, float2 sc, float2 z, u
   const float2 r = sub2(k, __half22float2(h));
   hi = h2_as_u32(h);
   lo = e5m2x2(r.x, r.y);
-}
-
-// Byte offset of element (r, k) of a [rows][128] 8-bit K-major operand in the
-// 128-byte-swizzled layout (one 128-byte row per r).
-__device__ __forceinline__ uint32_t sw128_offset_b8(int r, int k) {
-  return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((((k >> 4) ^ (r & 7))) << 4) + (k & 15));
 }
 
 // The rows of sequence b that the chunk holds, checked against the cache.
@@ -344,7 +266,7 @@ __global__ void __launch_bounds__(kOpThreads) prefill_operands_kernel(const Pref
       split_key(codes, make_float2(ks0, ks1), make_float2(kz0, kz1), hi, lo);
       const int key = dpage * 16 + t;  // within the half tile
       sts32(sK + tc05::sw128_offset(key, c0, kKeyTile / 2), hi);
-      sts16(sKlo + sw128_offset_b8(key, c0), lo);
+      sts16(sKlo + tc05::sw128_offset_b8(key, c0), lo);
       const __half vs = vscale[value_scale_slot(t, g)], vz = vzero[g * kPage + t];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -382,7 +304,7 @@ __global__ void __launch_bounds__(kOpThreads) prefill_operands_kernel(const Pref
         sts64(sK + ko, hi0, hi2);
         sts64(sK + ko + 1024, hi1, hi3);
         // tokens dn and dn + 8 are 8 rows (1024 bytes) apart in both layouts
-        const uint32_t ko8 = sw128_offset_b8(dpage * 16 + dn, c0);
+        const uint32_t ko8 = tc05::sw128_offset_b8(dpage * 16 + dn, c0);
         sts32(sKlo + ko8, static_cast<uint32_t>(lo0) | (static_cast<uint32_t>(lo2) << 16));
         sts32(sKlo + ko8 + 1024, static_cast<uint32_t>(lo1) | (static_cast<uint32_t>(lo3) << 16));
       }
@@ -416,7 +338,7 @@ __global__ void __launch_bounds__(kOpThreads) prefill_operands_kernel(const Pref
       if (tk < rres) kb = *reinterpret_cast<const uint32_t *>(rk + tk * kHeadDim + c);
       // residual keys are fp16 already: K_lo is zero
       sts32(sK + tc05::sw128_offset(dpage * 16 + tk, c, kKeyTile / 2), kb);
-      sts16(sKlo + sw128_offset_b8(dpage * 16 + tk, c), 0);
+      sts16(sKlo + tc05::sw128_offset_b8(dpage * 16 + tk, c), 0);
     }
     for (int e = widx; e < kPage * kHeadDim; e += 64) {
       const int tk = e >> 7, c = e & 127;
@@ -536,7 +458,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const PrefillPara
         for (int i = 0; i < 4; ++i)
           w[i] = static_cast<uint32_t>(e5m2x2_of_f16x2(v[8 * cc + 2 * i])) |
                  (static_cast<uint32_t>(e5m2x2_of_f16x2(v[8 * cc + 2 * i + 1])) << 16);
-        sts128(base + kOffQ8 + sw128_offset_b8(r, 16 * (4 * hc + cc)), make_uint4(w[0], w[1], w[2], w[3]));
+        sts128(base + kOffQ8 + tc05::sw128_offset_b8(r, 16 * (4 * hc + cc)), make_uint4(w[0], w[1], w[2], w[3]));
       }
     }
     tc05::tmem_wait_st();

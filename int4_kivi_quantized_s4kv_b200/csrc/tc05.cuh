@@ -23,6 +23,12 @@ __host__ __device__ __forceinline__ uint32_t sw128_offset(int r, int k, int rows
                                (((kk >> 3) ^ (r & 7)) << 4) + (kk & 7) * 2);
 }
 
+// Byte offset of element (r, k) of a [rows][128] 8-bit K-major operand in the
+// 128-byte-swizzled layout (one 128-byte row per r).
+__device__ __forceinline__ uint32_t sw128_offset_b8(int r, int k) {
+  return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((((k >> 4) ^ (r & 7))) << 4) + (k & 15));
+}
+
 // Shared-memory matrix descriptor: start address, stride between 8-row atoms
 // (1024 bytes), the sm_100 descriptor version and the 128-byte swizzle mode.
 // The leading-byte offset is not used by swizzled K-major operands.
@@ -47,6 +53,37 @@ __host__ __device__ constexpr uint32_t idesc_e5m2_f32(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
+
+// Descriptor of a K-major operand without swizzle, 16 k wide: 8 x 16-byte core
+// matrices (128 bytes), the two along k adjacent (leading-byte offset 128), the
+// next 8 rows behind them (stride 256).
+__device__ __forceinline__ uint64_t smem_desc_plain16(uint32_t addr) {
+  uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(128 >> 4) << 16;
+  d |= static_cast<uint64_t>(256 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+// Byte offset of element (r, k), k < 16, of such an fp16 operand.
+__host__ __device__ __forceinline__ uint32_t plain16_offset(int r, int k) {
+  return static_cast<uint32_t>((r >> 3) * 256 + (k >> 3) * 128 + (r & 7) * 16 + (k & 7) * 2);
+}
+
+// Descriptor of a 64-column fp16 operand that lies k-row by k-row (its 64 columns
+// contiguous, "MN-major") with the 128-byte swizzle: 8 rows make an atom of 1024
+// bytes, in which the 16-byte chunk c of row k sits at position c ^ (k % 8).
+__device__ __forceinline__ uint64_t smem_desc_mn64(uint32_t addr) {
+  uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1024 >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// Instruction-descriptor bit of a B operand that is MN-major.
+constexpr uint32_t kIdescMnB = 1u << 16;
 
 // Tensor-memory allocation (one whole warp executes these).  The allocated
 // base address is written to shared memory at `slot`.
@@ -96,6 +133,27 @@ __device__ __forceinline__ void mma_e5m2_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] . B[smem]^T, kind::f16 (K = 16 per MMA).
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] . B[smem]^T, kind::f8f6f4: row r of A in lane r, elements
+// 4c .. 4c + 3 of the row in column c, the lowest k in the lowest byte.
+__device__ __forceinline__ void mma_e5m2_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on `bar` when every MMA the elected lane issued so far
 // completes.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -126,6 +184,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
       "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
       "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+// Operand fragments into 16 lanes of tensor memory: register pair (2j, 2j + 1)
+// goes to columns 4j .. 4j + 3; lane 4n + i of the warp holds column 4j + i of rows n
+// (the first of the pair) and n + 8 -- where mma.m16n8k16's A registers 0, 1 and
+// 2, 3 lie.  taddr names the first of the 16 lanes.
+__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 

@@ -7,132 +7,933 @@
 // over the cached tokens (full pages dequantized, code * scale + zero; the
 // partial page from the fp16 residual), the node's ancestors and the node.
 //
-// One CTA takes eight query rows of a (sequence, kv head) over all its keys, 16
-// at a time, in fp32 with an online softmax.
-#include "code_map.cuh"
+// Work.  A unit is 64 query rows (node, head of the group) of a (sequence, kv
+// head); its keys come in tiles of 128: tile 0 holds the drafted tokens (64) and the
+// residual rows (16), tile t >= 1 the pages 8(t-1) .. 8t-1.  The tiles of all units
+// are laid end to end and cut into one contiguous range a CTA (one persistent CTA
+// an SM), so that one long sequence fills the card; a unit cut between CTAs leaves
+// partial results, and the CTA that finishes its last piece merges them.
+//
+// Tile.  Everything stands transposed: tokens (keys) or channels (values) on the
+// MMA's M = 128, query rows on N = 64, so that few rows cost little and both
+// dequantized operands are A operands, which live in tensor memory:
+//   S^T[token][row]   = K Q^T       K: lane = token,   from 4 K warps
+//   O^T[channel][row] += V^T P^T    V: lane = channel, from 4 V warps
+// A page's code words are mma fragments, and tcgen05.st's 16-lane shape lays a
+// fragment's registers down as they come, so unpacking a page is the same
+// straight-line code as in decode attention and no dequantized byte goes through
+// shared memory.  Keys: S = sum q (code scale) + sum q zero.  code/4 * scale is kept as
+// its fp16 rounding and the exact remainder, rounded to e5m2 (a second, fp8 MMA
+// against an e5m2 copy of q): the factor 1/4 keeps any fp16 range finite, and a
+// key is carried to about 2^-14 of code * scale, as in prefill attention.  The zero
+// points' share is one number a (page, row): two helper warps compute it with
+// mma.sync (8 pages x 64 rows) and hand it over as an fp16 hi + lo pair, which one
+// more MMA with a constant one-hot operand (token -> page) adds to S.  Values:
+// code * scale + zero, rounded once to fp16.  Weights enter as fp16 hi + lo.
+// What is left of the error is the values' rounding, as large as the output's own.
+//
+// Softmax.  Two groups of 4 warps take 32 query rows each; a thread is a token.  The
+// reference of a row moves only when a weight would pass 2^8: a vote of the group
+// decides; moving it (a maximum over the 128 tokens by redux, the sums and O
+// rescaled) is rare after a piece's first tile.
+//
+// Bound by HBM when R = nodes x G is small (176 bytes of int4 cache a token feed 512 R
+// operations), by the MMAs and the shared-memory port for many rows.
 #include "kernels.cuh"
+#include "tc05.cuh"
 
 namespace s4kv {
 
 namespace {
-constexpr int kRowsT = 8;
+
+// warps: K 0-3, V 4-7 and softmax 8-15 (their number mod 4 is the quarter of the
+// tensor-memory lanes that they reach), then the single ones
+constexpr int kVWarp0 = 4, kSoftmaxWarp0 = 8, kPageWarp = 16, kMmaWarp = 17, kHelpWarp0 = 18;
+constexpr int kTreeThreads = 32 * 20;  // 5 warps a scheduler: 96 registers a thread
+constexpr int kTile = 128;                 // keys a tile
+constexpr int kTilePages = kTile / kPage;  // 8
+constexpr int kGroupRows = 32;             // query rows of a softmax group
+#ifndef S4KV_TREE_MIN_TILES
+#define S4KV_TREE_MIN_TILES 2  // the fewest tiles a CTA is given
+#endif
+constexpr float kRefSlack = 8.0f;          // log2 slack of the softmax reference
+constexpr float kZeroUnit = 0x1p-10f;      // zero-point shares enter as share * 2^-10 (fp16) against 2^8, in units of 4
+
+constexpr uint32_t kIdescTS = tc05::idesc_f16_f32(128, kTreeRows);
+constexpr uint32_t kIdescTS8 = tc05::idesc_e5m2_f32(128, kTreeRows);
+constexpr uint32_t kIdescTO = tc05::idesc_f16_f32(128, kTreeRows) | tc05::kIdescMnB;
+
+// tensor memory, all 512 columns: S [2], O, K hi [2], V [2], K lo [2]
+constexpr uint32_t kTmS = 0, kTmO = 128, kTmKhi = 192, kTmV = 320, kTmKlo = 448;
+
+// shared memory
+constexpr uint32_t kQHiBytes = kTreeRows * 256, kQ8Bytes = kTreeRows * 128, kPBytes = kTile * kTreeRows * 2;
+constexpr uint32_t kOffQHi = 0;                              // [2]
+constexpr uint32_t kOffP = kOffQHi + 2 * kQHiBytes;          // [2][hi, lo]
+constexpr uint32_t kOffQ8 = kOffP + 4 * kPBytes;             // [2]
+constexpr uint32_t kOffHot = kOffQ8 + 2 * kQ8Bytes;          // one-hot operand [128][16]
+constexpr uint32_t kOffZero = kOffHot + kTile * 32;          // [2] zero-point operand [64][16]
+constexpr uint32_t kOffRef = kOffZero + 2 * kTreeRows * 32;  // minus the reference, [2][32] fp32
+constexpr uint32_t kOffRed = kOffRef + 2 * 32 * 4;           // [2][4][32] fp32
+constexpr uint32_t kOffFlag = kOffRed + 2 * 4 * 32 * 4;      // [2] last-piece flags, tensor memory's address, abort
+constexpr uint32_t kOffBar = kOffFlag + 16;
+constexpr uint32_t kBars = 32;
+constexpr uint32_t kOffRing = kOffBar + 8 * kBars;
+static_assert(kOffQ8 % 1024 == 0 && kOffRing % 16 == 0, "operand alignment");
+
+template <int kBits>
+struct Ring {
+  // pages 16 bytes apart, so that the same word of the 8 pages lies in 8 banks
+  static constexpr uint32_t kPageStride = Fmt<kBits>::kBlock + 16;
+  static constexpr uint32_t kStage = kTilePages * kPageStride;
+  static constexpr int kStages = kBits == 8 ? 2 : kBits == 2 ? 6 : 4;
+  static constexpr uint32_t kSmem = kOffRing + kStages * kStage + 1024;
+};
+static_assert(Ring<4>::kSmem <= 227 * 1024 && Ring<8>::kSmem <= 227 * 1024 && Ring<2>::kSmem <= 227 * 1024, "smem");
+
+// A sequence's share of the work; n = 0 where it has none.
+struct TreeSeq {
+  int c0, n, L, tiles, blocks;
+  uint32_t bad;
+};
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b) {
+  TreeSeq s;
+  s.c0 = __ldg(p.cu_nodes + b);
+  const int c1 = __ldg(p.cu_nodes + b + 1);
+  s.L = __ldg(p.seq_lens + b);
+  s.bad = 0;
+  s.n = 0;
+  if (s.c0 < 0 || c1 < s.c0 || c1 > p.n_nodes || c1 - s.c0 > p.max_nodes) s.bad = S4KV_EFLAG_TREE;
+  else if (c1 > s.c0 && (s.L < 0 || s.L > p.max_pages * kPage)) s.bad = S4KV_EFLAG_SEQ_LEN;
+  else s.n = c1 - s.c0;
+  s.tiles = s.n > 0 ? 1 + (s.L / kPage + kTilePages - 1) / kTilePages : 0;
+  s.blocks = (s.n * p.group + kTreeRows - 1) / kTreeRows;
+  return s;
 }
 
-__global__ void __launch_bounds__(128) tree_kernel(const TreeParams p) {
-  __shared__ float ks[kPage][kHeadDim + 1], vs[kPage][kHeadDim], qs[kRowsT][kHeadDim];
-  __shared__ float ss[kRowsT][kPage];
-  __shared__ unsigned long long anc[kRowsT];
-  const int b = blockIdx.y, h = blockIdx.z, tid = threadIdx.x, H = p.num_kv_heads, G = p.group;
-  const int c0 = __ldg(p.cu_nodes + b), c1 = __ldg(p.cu_nodes + b + 1), n = c1 - c0;
-  const bool first = blockIdx.x == 0 && h == 0 && tid == 0;
-  if (c0 < 0 || n < 0 || c1 > p.n_nodes || n > p.max_nodes) {
-    if (first) flag_error(p.err, S4KV_EFLAG_TREE);
-    return;
+// A warp's place in the flattened (sequence, kv head, row block, tile) order.
+struct TreeWalk {
+  TreeSeq s;
+  int b, h, rb;
+  int tile, rem;    // first tile of the current piece, tiles left from it on
+  long long start;  // flattened index of the unit's tile 0
+  __device__ __forceinline__ int take() const { return min(rem, s.tiles - tile); }
+  __device__ __forceinline__ int pages(int t) const { return min(kTilePages, s.L / kPage - kTilePages * (t - 1)); }
+  __device__ __forceinline__ void next(const TreeParams &p) {
+    const int t = take();
+    rem -= t;
+    start += s.tiles;
+    tile = 0;
+    if (rem <= 0) return;
+    if (++rb < s.blocks) return;
+    rb = 0;
+    if (++h < p.num_kv_heads) return;
+    h = 0;
+    do {
+      s = tree_seq(p, ++b);
+    } while (s.n == 0 && b + 1 < p.batch);
   }
-  const int L = __ldg(p.seq_lens + b);
-  if (n == 0) return;
-  if (L < 0 || L > p.max_pages * kPage) {
-    if (first) flag_error(p.err, S4KV_EFLAG_SEQ_LEN);
-    return;
-  }
-  const int r0 = blockIdx.x * kRowsT, rows = min(kRowsT, n * G - r0);
-  if (rows <= 0) return;
-  if (tid < rows) {
-    unsigned long long m = 0;
-    for (int a = (r0 + tid) / G; a >= 0;) {
-      m |= 1ull << a;
-      const int up = __ldg(p.parents + c0 + a);
-      if (up < -1 || up >= a) {
-        flag_error(p.err, S4KV_EFLAG_TREE);
-        break;
-      }
-      a = up;
+};
+
+// CTA whose range [c T / W, (c+1) T / W) holds tile x (W <= T).
+__device__ __forceinline__ long long cta_of(long long x, long long T, long long W) { return ((x + 1) * W + T - 1) / T - 1; }
+
+__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u), "r"(id)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float redux_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) { return h2_as_u32(__hmul2(u32_as_h2(a), u32_as_h2(b))); }
+__device__ __forceinline__ uint32_t hneg2_u32(uint32_t a) { return a ^ 0x80008000u; }
+
+// Exactly code / 4 from tile_codes' units, and the codes themselves.
+template <int kBits>
+__device__ __forceinline__ uint32_t quarter_unit() { return kBits == 4 ? 0x58005800u : 0x34003400u; }  // 128 (codes come as code / 512), 1/4
+template <int kBits>
+__device__ __forceinline__ void tile_codes(uint32_t w0, uint32_t w1, int parity, uint32_t (&a)[4]) {
+  if (kBits == 4) unpack_codes_s9(w0, a[0], a[1], a[2], a[3]);
+  else if (kBits == 8) unpack_codes8(w0, w1, a[0], a[1], a[2], a[3]);
+  else if (parity) unpack_codes2<1>(w0, a[0], a[1], a[2], a[3]);
+  else unpack_codes2<0>(w0, a[0], a[1], a[2], a[3]);
+}
+
+}  // namespace
+
+template <int kBits>
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams p) {
+  using F = Fmt<kBits>;
+  using R = Ring<kBits>;
+  constexpr unsigned kAll = 0xFFFFFFFFu;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *sm = smem_raw + (base - raw);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffFlag + 12);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = p.num_kv_heads, G = p.group, B = p.batch;
+
+  // barriers: a count of uses gives each its phase
+  auto bar = [&](int i) { return base + kOffBar + 8u * i; };
+  auto full = [&](int s) { return bar(s); };        // page stages
+  auto empty = [&](int s) { return bar(6 + s); };
+  auto k_ready = [&](int x) { return bar(12 + x); };  // K and the zero-point operand written
+  auto k_free = [&](int x) { return bar(14 + x); };
+  auto v_ready = [&](int x) { return bar(16 + x); };
+  auto v_free = [&](int x) { return bar(18 + x); };
+  auto s_full = [&](int x) { return bar(20 + x); };
+  auto s_free = [&](int x) { return bar(22 + x); };
+  auto p_full = [&](int x) { return bar(24 + x); };
+  auto p_free = [&](int x) { return bar(26 + x); };
+  auto q_full = [&](int x) { return bar(28 + x); };
+  auto q_free = [&](int x) { return bar(30 + x); };
+
+  // ---- plan: every warp finds this CTA's range for itself
+  TreeWalk w;
+  long long T, W;
+  {
+    const int per = (B + 31) >> 5;
+    const int b_lo = min(B, lane * per), b_hi = min(B, b_lo + per);
+    long long sum = 0;
+    uint32_t bad = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const TreeSeq s = tree_seq(p, b);
+      bad |= s.bad;
+      sum += static_cast<long long>(s.tiles) * s.blocks * H;
     }
-    anc[tid] = m;
-  }
-  for (int r = 0; r < kRowsT; ++r)
-    qs[r][tid] = r < rows ? __half2float(p.q[(static_cast<long>(c0 + (r0 + r) / G) * p.num_q_heads + h * G + (r0 + r) % G) * kHeadDim + tid]) : 0.f;
-  float O[kRowsT], mref[kRowsT], l[kRowsT];
-  for (int r = 0; r < kRowsT; ++r) {
-    O[r] = l[r] = 0.f;
-    mref[r] = -INFINITY;
-  }
-  const int nfull = L / kPage, res = L % kPage;
-  const int tiles = nfull + (res ? 1 : 0) + (n + kPage - 1) / kPage;
-  const int code_bytes = kPage * kHeadDim * p.bits / 8;
-  for (int tile = 0; tile < tiles; ++tile) {
-    __syncthreads();
-    int count = kPage, node0 = -1;
-    if (tile < nfull) {
-      int phys = __ldg(p.block_tables + static_cast<long>(b) * p.max_pages + tile);
-      if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_pages)) {
-        if (tid == 0) flag_error(p.err, S4KV_EFLAG_PAGE_RANGE);
-        phys = 0;
-      }
-      const uint8_t *blk = p.pool + (static_cast<long>(phys) * H + h) * block_bytes_for(p.bits);
-      const __half *meta = reinterpret_cast<const __half *>(blk + 2 * code_bytes);
-      const int c = tid, g = c / kVGroup;
-      const float sk = __half2float(meta[c]), zk = __half2float(meta[kHeadDim + key_zero_slot(c)]);
-      for (int t = 0; t < kPage; ++t) {
-        int w, j;
-        key_position(t, c, w, j);
-        ks[t][c] = static_cast<float>(code_at(blk, w, j, p.bits)) * sk + zk;
-        value_position(t, c, w, j);
-        vs[t][c] = static_cast<float>(code_at(blk + code_bytes, w, j, p.bits)) *
-                       __half2float(meta[2 * kHeadDim + value_scale_slot(t, g)]) +
-                   __half2float(meta[2 * kHeadDim + 64 + g * kPage + t]);
-      }
-    } else if (tile == nfull && res) {
-      count = res;
-      const long base = (static_cast<long>(b) * H + h) * kPage * kHeadDim + tid;
-      for (int t = 0; t < count; ++t) {
-        ks[t][tid] = __half2float(p.res_k[base + t * kHeadDim]);
-        vs[t][tid] = __half2float(p.res_v[base + t * kHeadDim]);
-      }
-    } else {
-      node0 = (tile - nfull - (res ? 1 : 0)) * kPage;
-      count = min(kPage, n - node0);
-      for (int t = 0; t < count; ++t) {
-        const long at = (static_cast<long>(c0 + node0 + t) * H + h) * kHeadDim + tid;
-        ks[t][tid] = __half2float(p.k[at]);
-        vs[t][tid] = __half2float(p.v[at]);
+    if (blockIdx.x == 0 && warp == 0 && bad) flag_error(p.err, bad);
+    long long incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long t = __shfl_up_sync(kAll, incl, off);
+      if (lane >= off) incl += t;
+    }
+    T = __shfl_sync(kAll, incl, 31);
+    W = max(1LL, min(static_cast<long long>(p.num_ctas), (T + S4KV_TREE_MIN_TILES - 1) / S4KV_TREE_MIN_TILES));
+    if (blockIdx.x >= W || T == 0) return;  // the whole CTA
+    const long long s0 = blockIdx.x * T / W, s1 = (blockIdx.x + 1) * T / W;
+    const long long excl = incl - sum;
+    const unsigned hit = __ballot_sync(kAll, excl <= s0 && s0 < incl);
+    const int src = __ffs(hit) - 1;
+    int bs = 0;
+    long long pre = excl;
+    if (lane == src) {
+      for (bs = b_lo; bs < b_hi; ++bs) {
+        const TreeSeq s = tree_seq(p, bs);
+        const long long mine = static_cast<long long>(s.tiles) * s.blocks * H;
+        if (s0 < pre + mine) break;
+        pre += mine;
       }
     }
-    __syncthreads();
-    {
-      const int r = tid >> 4, t = tid & 15;
-      float s = 0.f;
-      bool seen = r < rows && t < count;
-      if (seen && node0 >= 0) seen = (anc[r] >> (node0 + t)) & 1;
-      if (seen)
-        for (int c = 0; c < kHeadDim; ++c) s += qs[r][c] * ks[t][c];
-      ss[r][t] = seen ? s * p.scale_log2 : -INFINITY;
+    w.b = __shfl_sync(kAll, bs, src);
+    pre = __shfl_sync(kAll, pre, src);
+    w.s = tree_seq(p, w.b);
+    const long long u = (s0 - pre) / w.s.tiles;
+    w.h = static_cast<int>(u / w.s.blocks);
+    w.rb = static_cast<int>(u % w.s.blocks);
+    w.start = pre + u * w.s.tiles;
+    w.tile = static_cast<int>(s0 - w.start);
+    w.rem = static_cast<int>(s1 - s0);
+  }
+
+  // ---- setup
+  if (warp == kMmaWarp) {
+    tc05::tmem_alloc(base + kOffFlag + 8, 512);
+    tc05::tmem_relinquish();
+    tc05::fence_before_sync();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < R::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 10);  // K, V and helper warps
     }
-    __syncthreads();
-    for (int r = 0; r < rows; ++r) {
-      float m = mref[r];
-      for (int t = 0; t < count; ++t) m = fmaxf(m, ss[r][t]);
-      if (m == -INFINITY) continue;
-      const float a = exp2f(mref[r] - m);
-      O[r] *= a;
-      l[r] *= a;
-      mref[r] = m;
-      for (int t = 0; t < count; ++t) {
-        const float w = exp2f(ss[r][t] - m);
-        l[r] += w;
-        O[r] += w * vs[t][tid];
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(k_ready(x), 6);  // K and helper warps
+      mbar_init(k_free(x), 1);
+      mbar_init(v_ready(x), 4);
+      mbar_init(v_free(x), 1);
+      mbar_init(s_full(x), 1);
+      mbar_init(s_free(x), 8);
+      mbar_init(p_full(x), 8);
+      mbar_init(p_free(x), 1);
+      mbar_init(q_full(x), 2);
+      mbar_init(q_free(x), 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  // the one-hot operand: token t counts the shares (hi and lo) of page t / 16, times 2^8
+  for (int i = tid; i < kTile * 8; i += kTreeThreads) {
+    const int t = i >> 3, k = 2 * (i & 7);
+    uint32_t v = 0;
+    if ((k & 7) == (t / kPage & ~1)) v = (t / kPage & 1) ? 0x5C000000u : 0x00005C00u;
+    sts32(base + kOffHot + tc05::plain16_offset(t, k), v);
+  }
+  fence_proxy_async();
+  __syncthreads();
+  tc05::fence_after_sync();
+  const uint32_t tmem = lds32_at(base + kOffFlag + 8);
+  bool failed = false;
+  auto fail = [&]() {
+    failed = true;
+    *abort_flag = 1;
+  };
+  auto wait_warp = [&](uint32_t b_, uint32_t parity) { return __all_sync(kAll, wait_bounded(b_, parity, abort_flag)); };
+  // the phase of the use before the one of count k, of two buffers in turn
+  auto prev2 = [](int k) { return static_cast<uint32_t>(((k >> 1) - 1) & 1); };
+
+  if (warp == kPageWarp) {
+    // ------------------------------------------------- pages into the ring
+    int k = 0;  // stages filled
+    while (w.rem > 0 && !failed) {
+      const int t1 = w.tile + w.take();
+      const int32_t *bt = p.block_tables + static_cast<long>(w.b) * p.max_pages;
+      const uint8_t *head = p.pool + static_cast<long long>(w.h) * F::kBlock;
+      const int t0 = max(w.tile, 1);
+      // the ids of a tile are read while the stage of the tile before is waited for
+      int id = 0;
+      if (t0 < t1 && lane < w.pages(t0)) id = __ldg(bt + kTilePages * (t0 - 1) + lane);
+      for (int t = t0; t < t1; ++t, ++k) {
+        const int np = w.pages(t), st = k % R::kStages;
+        int phys = id;
+        if (t + 1 < t1 && lane < w.pages(t + 1)) id = __ldg(bt + kTilePages * t + lane);
+        if (k >= R::kStages && !wait_warp(empty(st), (k / R::kStages - 1) & 1)) {
+          fail();
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full(st), np * F::kBlock);
+        __syncwarp();
+        if (lane < np) {
+          if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_pages)) {
+            flag_error(p.err, S4KV_EFLAG_PAGE_RANGE);
+            phys = 0;
+          }
+          bulk_copy_g2s(base + kOffRing + st * R::kStage + lane * R::kPageStride,
+                        head + static_cast<long long>(phys) * H * F::kBlock, F::kBlock, full(st));
+        }
       }
+      w.next(p);
+    }
+    // before the CTA exits the copies in flight must have landed, after an abort too
+    for (int j = max(0, k - R::kStages); j < k; ++j) wait_landed(full(j % R::kStages), (j / R::kStages) & 1);
+  } else if (warp < kSoftmaxWarp0 || warp >= kHelpWarp0) {
+    // ------------------------- K warps, V warps, helpers: a tile's operands
+    const int n = lane >> 2, i = lane & 3;
+    const bool is_v = warp >= kVWarp0 && warp < kSoftmaxWarp0, is_help = warp >= kHelpWarp0;
+    const int wq = warp & 3;                  // K, V: quarter of the lanes
+    const int hw = warp - kHelpWarp0;         // helpers: rows 32 hw ..
+    const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
+    int k = 0, kt = 0, uc = 0;  // stages read, tiles, pieces
+    uint32_t qa[2][16], qb[2][16];  // helpers: query fragments of rows n and n + 8 of the two 16-row tiles
+    while (w.rem > 0 && !failed) {
+      const int t1 = w.tile + w.take();
+      if (is_help) {
+        // the unit's queries: rows to shared memory in the MMA's channel order (K hi: position 16 j + 8 e + 2 i + x
+        // holds channel 32 i + 4 j + 2 e + x; e5m2: position 16 j + 4 i + y channel 32 i + 4 j + y), fragments to registers
+        if (uc >= 2 && !wait_warp(q_free(uc & 1), prev2(uc))) {
+          fail();
+          break;
+        }
+        const int rows = w.s.n * G - kTreeRows * w.rb;
+        auto row_ptr = [&](int r) {
+          const int row = kTreeRows * w.rb + r;
+          return reinterpret_cast<const uint4 *>(
+              p.q + (static_cast<long>(w.s.c0 + row / G) * p.num_q_heads + w.h * G + row % G) * kHeadDim);
+        };
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        {
+          const int r = 32 * hw + lane;
+          const uint32_t qh = base + kOffQHi + (uc & 1) * kQHiBytes, q8 = base + kOffQ8 + (uc & 1) * kQ8Bytes;
+          const uint4 *src = row_ptr(r < rows ? r : 0);
+#pragma unroll 2
+          for (int t = 0; t < 4; ++t) {
+            uint4 x[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[c] = r < rows ? __ldg(src + 4 * c + t) : none;
+            // words of channels 32 c + 8 t ..: tiles 2t (x, y) and 2t + 1 (z, w)
+            sts128(qh + tc05::sw128_offset(r, 32 * t, kTreeRows), make_uint4(x[0].x, x[1].x, x[2].x, x[3].x));
+            sts128(qh + tc05::sw128_offset(r, 32 * t + 8, kTreeRows), make_uint4(x[0].y, x[1].y, x[2].y, x[3].y));
+            sts128(qh + tc05::sw128_offset(r, 32 * t + 16, kTreeRows), make_uint4(x[0].z, x[1].z, x[2].z, x[3].z));
+            sts128(qh + tc05::sw128_offset(r, 32 * t + 24, kTreeRows), make_uint4(x[0].w, x[1].w, x[2].w, x[3].w));
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              lo[c] = e5m2x2_of_f16x2(x[c].x) | static_cast<uint32_t>(e5m2x2_of_f16x2(x[c].y)) << 16;
+              hi[c] = e5m2x2_of_f16x2(x[c].z) | static_cast<uint32_t>(e5m2x2_of_f16x2(x[c].w)) << 16;
+            }
+            sts128(q8 + tc05::sw128_offset_b8(r, 32 * t), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            sts128(q8 + tc05::sw128_offset_b8(r, 32 * t + 16), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full(uc & 1));
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int ra = 32 * hw + 16 * m + n, rbb = ra + 8;
+          const uint4 *sa = row_ptr(ra < rows ? ra : 0) + 4 * i, *sb = row_ptr(rbb < rows ? rbb : 0) + 4 * i;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 x = ra < rows ? __ldg(sa + c) : none, y = rbb < rows ? __ldg(sb + c) : none;
+            qa[m][4 * c] = x.x; qa[m][4 * c + 1] = x.y; qa[m][4 * c + 2] = x.z; qa[m][4 * c + 3] = x.w;
+            qb[m][4 * c] = y.x; qb[m][4 * c + 1] = y.y; qb[m][4 * c + 2] = y.z; qb[m][4 * c + 3] = y.w;
+          }
+        }
+      }
+      for (int t = w.tile; t < t1; ++t, ++kt) {
+        const int x2 = kt & 1;
+        if (kt >= 2 && !wait_warp(is_v ? v_free(x2) : k_free(x2), prev2(kt))) {
+          fail();
+          break;
+        }
+        tc05::fence_after_sync();
+        const uint32_t tKhi = tmem + kTmKhi + 64u * x2, tKlo = tmem + kTmKlo + 32u * x2, tV = tmem + kTmV + 64u * x2;
+        if (t > 0) {
+          const int np = w.pages(t), st = k % R::kStages;
+          const uint32_t stage = base + kOffRing + st * R::kStage;
+          if (!wait_warp(full(st), (k / R::kStages) & 1)) {
+            fail();
+            break;
+          }
+          ++k;
+          if (is_help) {
+            float acc[2][4] = {};
+            const uint32_t z = stage + n * R::kPageStride + F::kKZero + 4 * i;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t b0 = n < np ? lds32_at(z + 32 * j) : 0u, b1 = n < np ? lds32_at(z + 32 * j + 16) : 0u;
+#pragma unroll
+              for (int m = 0; m < 2; ++m) mma16816(acc[m], qa[m][2 * j], qb[m][2 * j], qa[m][2 * j + 1], qb[m][2 * j + 1], b0, b1);
+            }
+            // shares of pages 2i, 2i + 1 for rows n, n + 8: fp16 hi at k = page, lo at k = 8 + page
+            const uint32_t zo = base + kOffZero + x2 * (kTreeRows * 32);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float2 v = make_float2(acc[m][2 * e] * kZeroUnit, acc[m][2 * e + 1] * kZeroUnit);
+                const __half2 hi = __floats2half2_rn(v.x, v.y);
+                const float2 d = sub2(v, __half22float2(hi));
+                const int r = 32 * hw + 16 * m + 8 * e + n;
+                sts32(zo + tc05::plain16_offset(r, 2 * i), h2_as_u32(hi));
+                sts32(zo + tc05::plain16_offset(r, 8 + 2 * i), h2_as_u32(__floats2half2_rn(d.x, d.y)));
+              }
+            }
+          } else if (is_v) {
+            // pages in batches of 4; lanes 0-15 of the quarter: channels 32 wq + 4n + {0, 1}, 16-31: + {2, 3}
+#pragma unroll 1
+            for (int pb = 0; pb < kTilePages; pb += 4) {
+              uint32_t o0[16], o1[16];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t a[4] = {0, 0, 0, 0}, c[4] = {0, 0, 0, 0};
+                if (pb + j < np) {
+                  const uint32_t blk = stage + (pb + j) * R::kPageStride;
+                  const uint32_t s0 = lds32_at(blk + F::kVScale + 32 * i + 4 * wq), s1 = lds32_at(blk + F::kVScale + 32 * i + 16 + 4 * wq);
+                  const uint32_t z0 = lds32_at(blk + F::kVZero + 32 * wq + 4 * i), z1 = lds32_at(blk + F::kVZero + 32 * wq + 4 * i + 16);
+                  if (kBits == 8) {
+                    const uint4 cw = lds128_at(blk + F::kVCode + 512 * wq + 16 * lane);
+                    tile_codes<kBits>(cw.x, cw.y, 0, a);
+                    tile_codes<kBits>(cw.z, cw.w, 1, c);
+                  } else if (kBits == 4) {
+                    const uint2 cw = lds64_at(blk + F::kVCode + 512 * (wq >> 1) + 16 * lane + 8 * (wq & 1));
+                    tile_codes<kBits>(cw.x, 0, 0, a);
+                    tile_codes<kBits>(cw.y, 0, 1, c);
+                  } else {
+                    const uint32_t cw = lds32_at(blk + F::kVCode + 16 * lane + 4 * wq);
+                    tile_codes<kBits>(cw, 0, 0, a);
+                    tile_codes<kBits>(cw, 0, 1, c);
+                  }
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) {
+                    if (kBits == 4) {
+                      a[r] = hmul2_u32(a[r], 0x60006000u);  // * 512: the codes
+                      c[r] = hmul2_u32(c[r], 0x60006000u);
+                    }
+                    a[r] = hfma2_u32(a[r], r < 2 ? s0 : s1, r < 2 ? z0 : z1);
+                    c[r] = hfma2_u32(c[r], r < 2 ? s0 : s1, r < 2 ? z0 : z1);
+                  }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  o0[4 * j + r] = a[r];
+                  o1[4 * j + r] = c[r];
+                }
+              }
+              tc05::tmem_st_frag16(tV + lane_base + 8 * pb, o0);
+              tc05::tmem_st_frag16(tV + lane_base + (16u << 16) + 8 * pb, o1);
+            }
+          } else {
+            // two pages a warp, half of a page's tiles at a time
+#pragma unroll 1
+            for (int ph = 0; ph < 4; ++ph) {
+              const int pg = 2 * wq + (ph >> 1), hf = ph & 1;
+              if (pg >= np) break;  // the lanes of missing pages hold what they held: their logits are masked
+              const uint32_t blk = stage + pg * R::kPageStride, sc = blk + F::kKScale + 64 * i + 32 * hf;
+              const uint4 sa = lds128_at(sc), sb = lds128_at(sc + 16);
+              const uint32_t s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+              uint32_t cw[8];
+              if (kBits == 4) {
+                const uint4 c = lds128_at(blk + F::kKCode + 512 * hf + 16 * lane);
+                cw[0] = c.x; cw[1] = c.y; cw[2] = c.z; cw[3] = c.w;
+              } else if (kBits == 8) {
+                const uint4 c = lds128_at(blk + F::kKCode + 1024 * hf + 16 * lane), d = lds128_at(blk + F::kKCode + 1024 * hf + 512 + 16 * lane);
+                cw[0] = c.x; cw[1] = c.y; cw[2] = c.z; cw[3] = c.w;
+                cw[4] = d.x; cw[5] = d.y; cw[6] = d.z; cw[7] = d.w;
+              } else {
+                const uint2 c = lds64_at(blk + F::kKCode + 16 * lane + 8 * hf);
+                cw[0] = c.x; cw[1] = c.y;
+              }
+              uint32_t hi[16], lo[8];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t a[4];
+                tile_codes<kBits>(kBits == 8 ? cw[2 * q] : kBits == 4 ? cw[q] : cw[q >> 1], kBits == 8 ? cw[2 * q + 1] : 0, q & 1, a);
+                uint16_t l8[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  const uint32_t c4 = hmul2_u32(a[r], quarter_unit<kBits>()), sr = s[2 * q + (r >> 1)];
+                  const uint32_t hr = hmul2_u32(c4, sr);
+                  hi[4 * q + r] = hr;
+                  l8[r] = e5m2x2_of_f16x2(hfma2_u32(c4, sr, hneg2_u32(hr)));  // the exact remainder, rounded to e5m2
+                }
+                lo[2 * q] = l8[0] | static_cast<uint32_t>(l8[2]) << 16;
+                lo[2 * q + 1] = l8[1] | static_cast<uint32_t>(l8[3]) << 16;
+              }
+              const uint32_t at = lane_base + (static_cast<uint32_t>(16 * (ph >> 1)) << 16);
+              tc05::tmem_st_frag16(tKhi + at + 32 * hf, hi);
+              tc05::tmem_st_frag8(tKlo + at + 16 * hf, lo);
+            }
+          }
+          // the stage has been read
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty(st));
+        } else if (!is_help) {
+          // tile 0: tokens 0-63 the drafted ones, 64-79 the residual rows
+          const int r = w.s.L % kPage;
+          const long res_base = (static_cast<long>(w.b) * H + w.h) * kPage * kHeadDim;
+          auto rows_of = [&](int grp, const __half *x, const __half *res, int &count, long &stride) -> const __half * {
+            if (grp < 4) {
+              count = w.s.n - kPage * grp;
+              stride = static_cast<long>(H) * kHeadDim;
+              return x + (static_cast<long>(w.s.c0 + kPage * grp) * H + w.h) * kHeadDim;
+            }
+            count = grp == 4 ? r : 0;
+            stride = kHeadDim;
+            return res + res_base;
+          };
+          if (is_v) {
+#pragma unroll 1
+            for (int pb = 0; pb < kTilePages; pb += 4) {
+              uint32_t o0[16], o1[16];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                int count;
+                long stride;
+                const __half *rv = rows_of(pb + j, p.v, p.res_v, count, stride);
+                uint2 x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int tk = 2 * i + (e & 1) + 8 * (e >> 1);
+                  x[e] = tk < count ? *reinterpret_cast<const uint2 *>(rv + tk * stride + 32 * wq + 4 * n) : make_uint2(0, 0);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  o0[4 * j + 2 * e] = __byte_perm(x[2 * e].x, x[2 * e + 1].x, 0x5410);
+                  o0[4 * j + 2 * e + 1] = __byte_perm(x[2 * e].x, x[2 * e + 1].x, 0x7632);
+                  o1[4 * j + 2 * e] = __byte_perm(x[2 * e].y, x[2 * e + 1].y, 0x5410);
+                  o1[4 * j + 2 * e + 1] = __byte_perm(x[2 * e].y, x[2 * e + 1].y, 0x7632);
+                }
+              }
+              tc05::tmem_st_frag16(tV + lane_base + 8 * pb, o0);
+              tc05::tmem_st_frag16(tV + lane_base + (16u << 16) + 8 * pb, o1);
+            }
+          } else {
+#pragma unroll 1
+            for (int ph = 0; ph < 4; ++ph) {
+              const int grp = 2 * wq + (ph >> 1), hf = ph & 1;
+              int count;
+              long stride;
+              const __half *rk = rows_of(grp, p.k, p.res_k, count, stride) + 32 * i + 16 * hf;
+              uint32_t hi[16];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                if (n < count) x = *reinterpret_cast<const uint4 *>(rk + n * stride + 8 * c);
+                if (n + 8 < count) y = *reinterpret_cast<const uint4 *>(rk + (n + 8) * stride + 8 * c);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // in quarters, as the quantized keys
+                  hi[8 * c + 2 * e] = hmul2_u32(xs[e], 0x34003400u);
+                  hi[8 * c + 2 * e + 1] = hmul2_u32(ys[e], 0x34003400u);
+                }
+              }
+              tc05::tmem_st_frag16(tKhi + lane_base + (static_cast<uint32_t>(16 * (ph >> 1)) << 16) + 32 * hf, hi);
+            }
+          }
+        }
+        if (is_help) {
+          fence_proxy_async();
+        } else {
+          tc05::tmem_wait_st();
+          tc05::fence_before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(is_v ? v_ready(x2) : k_ready(x2));
+      }
+      ++uc;
+      w.next(p);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------- S^T(kt) = K Q^T, then O^T += V^T P^T of tile kt - 1
+    const uint64_t dhot = tc05::smem_desc_plain16(base + kOffHot);
+    int kt = 0, uc = 0;
+    bool fresh = true;  // tile kt - 1 starts a piece
+    auto issue_pv = [&](int k1) {
+      const int x2 = k1 & 1;
+      if (!wait_warp(v_ready(x2), (k1 >> 1) & 1) || !wait_warp(p_full(x2), (k1 >> 1) & 1)) return false;
+      tc05::fence_after_sync();
+      const uint64_t dhi = tc05::smem_desc_mn64(base + kOffP + (2 * x2) * kPBytes);
+      const uint64_t dlo = tc05::smem_desc_mn64(base + kOffP + (2 * x2 + 1) * kPBytes);
+      const uint32_t tV = tmem + kTmV + 64u * x2;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        tc05::mma_f16_ts(tmem + kTmO, tV + 8 * j, dhi + ((2048 * j) >> 4), kIdescTO, (!fresh || j > 0) ? 1u : 0u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) tc05::mma_f16_ts(tmem + kTmO, tV + 8 * j, dlo + ((2048 * j) >> 4), kIdescTO, 1u);
+      tc05::mma_commit(p_free(x2));
+      tc05::mma_commit(v_free(x2));
+      return true;
+    };
+    while (w.rem > 0 && !failed) {
+      const int t1 = w.tile + w.take();
+      const uint64_t dq = tc05::smem_desc_sw128(base + kOffQHi + (uc & 1) * kQHiBytes);
+      const uint64_t dq8 = tc05::smem_desc_sw128(base + kOffQ8 + (uc & 1) * kQ8Bytes);
+      for (int t = w.tile; t < t1; ++t, ++kt) {
+        const int x2 = kt & 1;
+        if ((t == w.tile && !wait_warp(q_full(uc & 1), (uc >> 1) & 1)) || !wait_warp(k_ready(x2), (kt >> 1) & 1) ||
+            (kt >= 2 && !wait_warp(s_free(x2), prev2(kt)))) {
+          fail();
+          break;
+        }
+        tc05::fence_after_sync();
+        const uint32_t tS = tmem + kTmS + 64u * x2, tKhi = tmem + kTmKhi + 64u * x2, tKlo = tmem + kTmKlo + 32u * x2;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          tc05::mma_f16_ts(tS, tKhi + 8 * j, dq + (((j >> 2) * (kQHiBytes / 2) + (j & 3) * 32) >> 4), kIdescTS, j > 0 ? 1u : 0u);
+        if (t > 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tc05::mma_e5m2_ts(tS, tKlo + 8 * j, dq8 + ((32 * j) >> 4), kIdescTS8, 1u);
+          tc05::mma_f16_ss(tS, dhot, tc05::smem_desc_plain16(base + kOffZero + x2 * (kTreeRows * 32)), kIdescTS, 1u);
+        }
+        tc05::mma_commit(s_full(x2));
+        tc05::mma_commit(k_free(x2));
+        if (t + 1 == t1) tc05::mma_commit(q_free(uc & 1));
+        if (kt > 0 && !issue_pv(kt - 1)) {
+          fail();
+          break;
+        }
+        fresh = t == w.tile;
+      }
+      ++uc;
+      w.next(p);
+    }
+    if (!failed && !issue_pv(kt - 1)) fail();
+  } else {
+    // ------------------------------------------- softmax and the output
+    const int g = (warp - kSoftmaxWarp0) >> 2, wq = warp & 3, tl = 32 * wq + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
+    const uint32_t s_ref = base + kOffRef + 128 * g;
+    float *red = reinterpret_cast<float *>(sm + kOffRed) + 128 * g;
+    volatile int *last_flag = reinterpret_cast<volatile int *>(sm + kOffFlag) + g;
+    const int bid = 1 + g;
+    const float sc = 4.0f * p.scale_log2;
+    const uint32_t tO = tmem + kTmO + 32u * g + lane_base;
+    bool ok = true;  // the group leaves together: a failed wait is told at the next vote
+    bool first_piece = true;
+    int kt = 0;
+    while (w.rem > 0 && !failed) {
+      const int t0 = w.tile, t1 = w.tile + w.take();
+      const int rows = min(kGroupRows, w.s.n * G - kTreeRows * w.rb - kGroupRows * g);  // of this group
+      float l[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) l[j] = 0.f;
+      float myref = -INFINITY;  // lane j: the reference of row j (every warp of the group holds the same)
+      if (rows > 0) {
+        if (wq == 0) reinterpret_cast<float *>(sm + kOffRef)[32 * g + lane] = INFINITY;
+        group_sync(bid);
+      }
+      uint32_t seen = 0;  // tile 0: the rows that see this token
+      if (t0 == 0 && rows > 0) {
+        // ancestors of nodes lane and lane + 32, themselves among them, by pointer doubling
+        int up[2];
+        unsigned long long anc[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int a = lane + 32 * e;
+          up[e] = a < w.s.n ? __ldg(p.parents + w.s.c0 + a) : -1;
+          if (up[e] < -1 || up[e] >= a) {
+            if (a < w.s.n) flag_error(p.err, S4KV_EFLAG_TREE);
+            up[e] = -1;
+          }
+          anc[e] = 1ull << a;
+        }
+#pragma unroll 1
+        for (int s = 0; s < 6; ++s) {
+          unsigned long long m[2];
+          int u[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const unsigned long long m0 = __shfl_sync(kAll, anc[0], up[e] & 31), m1 = __shfl_sync(kAll, anc[1], up[e] & 31);
+            const int u0 = __shfl_sync(kAll, up[0], up[e] & 31), u1 = __shfl_sync(kAll, up[1], up[e] & 31);
+            m[e] = up[e] < 0 ? 0ull : up[e] < 32 ? m0 : m1;
+            u[e] = up[e] < 0 ? -1 : up[e] < 32 ? u0 : u1;
+          }
+          anc[0] |= m[0];
+          anc[1] |= m[1];
+          up[0] = u[0];
+          up[1] = u[1];
+        }
+#pragma unroll 1
+        for (int j = 0; j < 32; ++j) {
+          const int node = j < rows ? (kTreeRows * w.rb + kGroupRows * g + j) / G : 0;
+          const unsigned long long m0 = __shfl_sync(kAll, anc[0], node & 31), m1 = __shfl_sync(kAll, anc[1], node & 31);
+          const unsigned long long m = node < 32 ? m0 : m1;
+          const bool s = tl < 64 ? (m >> tl) & 1 : tl - 64 < w.s.L % kPage;
+          seen |= (s ? 1u : 0u) << j;
+        }
+      }
+      for (int t = t0; t < t1; ++t, ++kt) {
+        const int x2 = kt & 1;
+        ok = ok && wait_warp(s_full(x2), (kt >> 1) & 1);
+        if (rows <= 0) {  // nothing to do but to keep the barriers' counts
+          ok = ok && (kt < 2 || wait_warp(p_free(x2), prev2(kt)));
+          if (!ok) {
+            fail();
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive(s_free(x2));
+            mbar_arrive(p_full(x2));
+          }
+          continue;
+        }
+        tc05::fence_after_sync();
+        uint32_t sv[32];
+        auto load = [&]() {
+          tc05::tmem_ld32(tmem + kTmS + 64u * x2 + 32u * g + lane_base, sv);
+          tc05::tmem_wait_ld();
+        };
+        // logits in log2 units minus the reference; -inf where this token is not seen
+        const uint32_t mask = t == 0 ? seen : (tl / kPage < w.pages(t) ? 0xFFFFFFFFu : 0u);
+        auto shift = [&]() {
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const uint4 r = lds128_at(s_ref + 4 * j);
+            float2 a = make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
+            float2 b = make_float2(__uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3]));
+            a = fma2(a, make_float2(sc, sc), make_float2(__uint_as_float(r.x), __uint_as_float(r.y)));
+            b = fma2(b, make_float2(sc, sc), make_float2(__uint_as_float(r.z), __uint_as_float(r.w)));
+            if (mask != 0xFFFFFFFFu) {
+              a.x = mask >> j & 1 ? a.x : -INFINITY;
+              a.y = mask >> (j + 1) & 1 ? a.y : -INFINITY;
+              b.x = mask >> (j + 2) & 1 ? b.x : -INFINITY;
+              b.y = mask >> (j + 3) & 1 ? b.y : -INFINITY;
+            }
+            m0 = fmax3(m0, a.x, a.y);
+            m1 = fmax3(m1, b.x, b.y);
+            sv[j] = __float_as_uint(a.x);
+            sv[j + 1] = __float_as_uint(a.y);
+            sv[j + 2] = __float_as_uint(b.x);
+            sv[j + 3] = __float_as_uint(b.y);
+          }
+          return fmaxf(m0, m1);
+        };
+        load();
+        const float top = shift();
+        if (group_any(bid, top > kRefSlack || !ok)) {
+          if (group_any(bid, !ok)) {
+            fail();
+            break;
+          }
+          // move references: the tile's maximum of each row, lane j keeps row j's
+          load();
+          float mine = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float m = redux_max(mask >> j & 1 ? __uint_as_float(sv[j]) * sc : -INFINITY);
+            if (lane == j) mine = m;
+          }
+          red[32 * wq + lane] = mine;
+          group_sync(bid);
+          mine = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));
+          const float now = mine > myref + kRefSlack ? mine : myref;
+          const float f = now == myref ? 1.0f : fast_exp2(myref - now);  // 0 where there was no reference yet
+          myref = now;
+          if (wq == 0) reinterpret_cast<float *>(sm + kOffRef)[32 * g + lane] = -now;
+          group_sync(bid);
+          if (t > t0) {
+            // the sums so far, and O once every product before this tile's is in it
+            ok = ok && wait_warp(p_free(x2 ^ 1), ((kt - 1) >> 1) & 1);
+            tc05::fence_after_sync();
+            uint32_t o[32];
+            tc05::tmem_ld32(tO, o);
+            tc05::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float fj = __shfl_sync(kAll, f, j);
+              l[j] *= fj;
+              o[j] = __float_as_uint(__uint_as_float(o[j]) * fj);
+            }
+            tc05::tmem_st32(tO, o);
+            tc05::tmem_wait_st();
+          }
+          load();
+          shift();
+        }
+        // S has been read
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free(x2));
+        ok = ok && (kt < 2 || wait_warp(p_free(x2), prev2(kt)));
+        const uint32_t ph = base + kOffP + (2 * x2) * kPBytes + (tl >> 3) * 1024 + (tl & 7) * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 8 * c + 2 * e;
+            const float2 x = make_float2(fast_exp2(__uint_as_float(sv[j])), fast_exp2(__uint_as_float(sv[j + 1])));
+            l[j] += x.x;
+            l[j + 1] += x.y;
+            const __half2 hh = __floats2half2_rn(x.x, x.y);
+            const float2 d = sub2(x, __half22float2(hh));
+            hi[e] = h2_as_u32(hh);
+            lo[e] = h2_as_u32(__floats2half2_rn(d.x, d.y));
+          }
+          const uint32_t at = ph + (((4 * g + c) ^ (tl & 7)) << 4);
+          sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(at + kPBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(x2));
+      }
+      if (failed) break;
+
+      // ---- the piece's end: sums over the tokens (lane j: row j), O once its last product is in it
+      if (rows > 0) {
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) {
+#pragma unroll
+          for (int j = 0; j < s; ++j) {
+            const bool up = lane & s;
+            const float keep = up ? l[j + s] : l[j], send = up ? l[j] : l[j + s];
+            l[j] = keep + __shfl_xor_sync(kAll, send, s);
+          }
+        }
+        red[32 * wq + lane] = l[0];
+        ok = ok && wait_warp(p_free((kt - 1) & 1), ((kt - 1) >> 1) & 1);
+        if (group_any(bid, !ok)) {
+          fail();
+          break;
+        }
+        const float lsum = red[lane] + red[32 + lane] + red[64 + lane] + red[96 + lane];
+        tc05::fence_after_sync();
+        uint32_t o[32];
+        tc05::tmem_ld32(tO, o);
+        tc05::tmem_wait_ld();
+        const int row0 = kTreeRows * w.rb + kGroupRows * g;
+        const int ch = 32 * wq + 4 * (lane & 7) + 2 * (lane >> 4) + (lane >> 3 & 1);  // the channel of this lane
+        auto out_ptr = [&](int row) {
+          return p.out + (static_cast<long>(w.s.c0 + row / G) * p.num_q_heads + w.h * G + row % G) * kHeadDim + ch;
+        };
+        if (t0 == 0 && t1 == w.s.tiles) {
+          const float inv = 1.0f / lsum;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float ij = __shfl_sync(kAll, inv, j);
+            if (j < rows) *out_ptr(row0 + j) = __float2half_rn(__uint_as_float(o[j]) * ij);
+          }
+        } else {
+          const long long slot = 2ll * blockIdx.x + (first_piece ? 0 : 1);
+          float *dst = p.part + (slot * kTreeRows + kGroupRows * g) * kHeadDim + ch;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j < rows) dst[j * kHeadDim] = __uint_as_float(o[j]);
+          if (wq == 0) p.part_ml[slot * kTreeRows + kGroupRows * g + lane] = make_float2(myref, lsum);
+          __threadfence();
+          group_sync(bid);
+          const long long wf = cta_of(w.start, T, W), wl = cta_of(w.start + w.s.tiles - 1, T, W);
+          const int rbs = (p.max_nodes * G + kTreeRows - 1) / kTreeRows;
+          uint32_t *ticket = p.tickets + ((static_cast<long>(w.b) * H + w.h) * rbs + w.rb) * 2 + g;
+          if (wq == 0 && lane == 0) {
+            const bool last = atomicAdd(ticket, 1u) + 1 == static_cast<uint32_t>(wl - wf + 1);
+            if (last) *ticket = 0u;
+            *last_flag = last;
+          }
+          group_sync(bid);
+          if (*last_flag) {
+            // merge the unit's pieces in their order; this thread owns a channel
+            __threadfence();
+            auto slot_of = [&](long long c) { return 2 * c + ((c == wf && c * T / W < w.start) ? 1 : 0); };
+            for (int j = 0; j < rows; ++j) {
+              float M = -INFINITY;
+              for (long long c = wf + lane; c <= wl; c += 32)
+                M = fmaxf(M, __ldcg(p.part_ml + slot_of(c) * kTreeRows + kGroupRows * g + j).x);
+              M = redux_max(M);
+              float acc = 0.f, sum = 0.f;
+#pragma unroll 4
+              for (long long c = wf; c <= wl; ++c) {
+                const long long at = slot_of(c) * kTreeRows + kGroupRows * g + j;
+                const float2 ml = __ldcg(p.part_ml + at);
+                const float wt = fast_exp2(ml.x - M);
+                sum += wt * ml.y;
+                acc += wt * __ldcg(p.part + at * kHeadDim + ch);
+              }
+              *out_ptr(row0 + j) = __float2half_rn(acc / sum);
+            }
+          }
+          group_sync(bid);  // the flag is read before another piece sets it
+        }
+      }
+      first_piece = false;
+      w.next(p);
     }
   }
-  for (int r = 0; r < rows; ++r)
-    p.out[(static_cast<long>(c0 + (r0 + r) / G) * p.num_q_heads + h * G + (r0 + r) % G) * kHeadDim + tid] =
-        __float2half_rn(O[r] / l[r]);
+
+  if (failed) flag_error(p.err, S4KV_EFLAG_TIMEOUT);
+  tc05::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc05::fence_after_sync();
+    tc05::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kBits>
+static cudaError_t launch_tree_for(const TreeParams &p, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(tree_kernel<kBits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(Ring<kBits>::kSmem));
+  if (e != cudaSuccess) return e;
+  tree_kernel<kBits><<<p.num_ctas, kTreeThreads, Ring<kBits>::kSmem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream) {
-  const dim3 grid((p.max_nodes * p.group + kRowsT - 1) / kRowsT, p.batch, p.num_kv_heads);
-  tree_kernel<<<grid, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  return p.bits == 8 ? launch_tree_for<8>(p, stream) : p.bits == 2 ? launch_tree_for<2>(p, stream) : launch_tree_for<4>(p, stream);
 }
 
 }  // namespace s4kv
