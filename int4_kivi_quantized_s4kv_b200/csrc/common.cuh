@@ -461,4 +461,23 @@ __device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity) {
   }
 }
 
+// The same with the waiting warp suspended by the barrier unit, up to a few
+// microseconds a try: a spinning warp would take issue slots from those at work.
+__device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, const volatile int *abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(4000)
+        : "memory");
+    if (done) return true;
+    if (*abort || clock64() - t0 > kAbortWaitCycles) return false;
+  }
+}
+
 }  // namespace s4kv

@@ -33,9 +33,9 @@
 // What is left of the error is the values' rounding, as large as the output's own.
 //
 // Softmax.  Two groups of 4 warps take 32 query rows each; a thread is a token.  The
-// reference of a row moves only when a weight would pass 2^8: a vote of the group
-// decides; moving it (a maximum over the 128 tokens by redux, the sums and O
-// rescaled) is rare after a piece's first tile.
+// reference of a row is the largest logit of a piece's first tile and moves only when a
+// weight would pass 2^14 (still finite in fp16): a vote of the group decides, and
+// moving it (a maximum over the 128 tokens, the sums and O rescaled) is rare.
 //
 // Bound by HBM when R = nodes x G is small (176 bytes of int4 cache a token feed 512 R
 // operations), by the MMAs and the shared-memory port for many rows.
@@ -56,7 +56,7 @@ constexpr int kGroupRows = 32;             // query rows of a softmax group
 #ifndef S4KV_TREE_MIN_TILES
 #define S4KV_TREE_MIN_TILES 2  // the fewest tiles a CTA is given
 #endif
-constexpr float kRefSlack = 8.0f;          // log2 slack of the softmax reference
+constexpr float kRefSlack = 14.0f;         // log2 slack of the softmax reference: weights up to 2^14, finite in fp16
 constexpr float kZeroUnit = 0x1p-10f;      // zero-point shares enter as share * 2^-10 (fp16) against 2^8, in units of 4
 
 constexpr uint32_t kIdescTS = tc05::idesc_f16_f32(128, kTreeRows);
@@ -76,7 +76,8 @@ constexpr uint32_t kOffZero = kOffHot + kTile * 32;          // [2] zero-point o
 constexpr uint32_t kOffRef = kOffZero + 2 * kTreeRows * 32;  // minus the reference, [2][32] fp32
 constexpr uint32_t kOffRed = kOffRef + 2 * 32 * 4;           // [2][4][32] fp32
 constexpr uint32_t kOffFlag = kOffRed + 2 * 4 * 32 * 4;      // [2] last-piece flags, tensor memory's address, abort
-constexpr uint32_t kOffBar = kOffFlag + 16;
+constexpr uint32_t kOffSplit = kOffFlag + 16;                  // the TreeSplit
+constexpr uint32_t kOffBar = kOffSplit + 16;
 constexpr uint32_t kBars = 32;
 constexpr uint32_t kOffRing = kOffBar + 8 * kBars;
 static_assert(kOffQ8 % 1024 == 0 && kOffRing % 16 == 0, "operand alignment");
@@ -135,8 +136,21 @@ struct TreeWalk {
   }
 };
 
-// CTA whose range [c T / W, (c+1) T / W) holds tile x (W <= T).
-__device__ __forceinline__ long long cta_of(long long x, long long T, long long W) { return ((x + 1) * W + T - 1) / T - 1; }
+// The tiles 0 .. T-1 in consecutive ranges of W CTAs: the first `extra` of them take
+// each + 1 tiles, the others `each`.
+struct TreeSplit {
+  long long each;
+  int extra;
+  __device__ __forceinline__ long long first(int c) const { return c * each + min(c, extra); }
+  __device__ __forceinline__ int cta_of(long long x) const {
+    const long long longer = extra * (each + 1);
+    return static_cast<int>(x < longer ? div(x, each + 1) : extra + div(x - longer, each));
+  }
+  // 64-bit quotients are slow and next to never needed
+  static __device__ __forceinline__ long long div(long long x, long long y) {
+    return ((x | y) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+  }
+};
 
 __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool group_any(int id, bool x) {
@@ -148,14 +162,23 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ float redux_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
+// Lane j's v[0] becomes the reduction over the warp's lanes of every lane's v[j];
+// the rest of v is used up.
+template <typename Op>
+__device__ __forceinline__ float warp_reduce_rows(float (&v)[32], int lane, Op op) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int j = 0; j < s; ++j) {
+      const float keep = up ? v[j + s] : v[j], send = up ? v[j] : v[j + s];
+      v[j] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, s));
+    }
+  }
+  return v[0];
 }
 
 __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) { return h2_as_u32(__hmul2(u32_as_h2(a), u32_as_h2(b))); }
-__device__ __forceinline__ uint32_t hneg2_u32(uint32_t a) { return a ^ 0x80008000u; }
 
 // Exactly code / 4 from tile_codes' units, and the codes themselves.
 template <int kBits>
@@ -200,7 +223,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 
   // ---- plan: every warp finds this CTA's range for itself
   TreeWalk w;
-  long long T, W;
   {
     const int per = (B + 31) >> 5;
     const int b_lo = min(B, lane * per), b_hi = min(B, b_lo + per);
@@ -218,10 +240,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       const long long t = __shfl_up_sync(kAll, incl, off);
       if (lane >= off) incl += t;
     }
-    T = __shfl_sync(kAll, incl, 31);
-    W = max(1LL, min(static_cast<long long>(p.num_ctas), (T + S4KV_TREE_MIN_TILES - 1) / S4KV_TREE_MIN_TILES));
-    if (blockIdx.x >= W || T == 0) return;  // the whole CTA
-    const long long s0 = blockIdx.x * T / W, s1 = (blockIdx.x + 1) * T / W;
+    const long long T = __shfl_sync(kAll, incl, 31);
+    const int W = static_cast<int>(min(static_cast<long long>(p.num_ctas), (T + S4KV_TREE_MIN_TILES - 1) / S4KV_TREE_MIN_TILES));
+    if (static_cast<int>(blockIdx.x) >= W) return;  // the whole CTA
+    TreeSplit split;
+    split.each = TreeSplit::div(T, W);
+    split.extra = static_cast<int>(T - split.each * W);
+    const long long s0 = split.first(blockIdx.x), s1 = split.first(blockIdx.x + 1);
+    if (tid == 0) *reinterpret_cast<TreeSplit *>(sm + kOffSplit) = split;  // for the merge of cut units
     const long long excl = incl - sum;
     const unsigned hit = __ballot_sync(kAll, excl <= s0 && s0 < incl);
     const int src = __ffs(hit) - 1;
@@ -238,10 +264,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     w.b = __shfl_sync(kAll, bs, src);
     pre = __shfl_sync(kAll, pre, src);
     w.s = tree_seq(p, w.b);
-    const long long u = (s0 - pre) / w.s.tiles;
-    w.h = static_cast<int>(u / w.s.blocks);
-    w.rb = static_cast<int>(u % w.s.blocks);
-    w.start = pre + u * w.s.tiles;
+    const int u = static_cast<int>(TreeSplit::div(s0 - pre, w.s.tiles));
+    w.h = u / w.s.blocks;
+    w.rb = u - w.h * w.s.blocks;
+    w.start = pre + static_cast<long long>(u) * w.s.tiles;
     w.tile = static_cast<int>(s0 - w.start);
     w.rem = static_cast<int>(s1 - s0);
   }
@@ -288,7 +314,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     failed = true;
     *abort_flag = 1;
   };
-  auto wait_warp = [&](uint32_t b_, uint32_t parity) { return __all_sync(kAll, wait_bounded(b_, parity, abort_flag)); };
+  auto wait_warp = [&](uint32_t b_, uint32_t parity) { return __all_sync(kAll, wait_suspended(b_, parity, abort_flag)); };
   // the phase of the use before the one of count k, of two buffers in turn
   auto prev2 = [](int k) { return static_cast<uint32_t>(((k >> 1) - 1) & 1); };
 
@@ -334,61 +360,40 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     const int hw = warp - kHelpWarp0;         // helpers: rows 32 hw ..
     const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
     int k = 0, kt = 0, uc = 0;  // stages read, tiles, pieces
-    uint32_t qa[2][16], qb[2][16];  // helpers: query fragments of rows n and n + 8 of the two 16-row tiles
     while (w.rem > 0 && !failed) {
       const int t1 = w.tile + w.take();
       if (is_help) {
-        // the unit's queries: rows to shared memory in the MMA's channel order (K hi: position 16 j + 8 e + 2 i + x
-        // holds channel 32 i + 4 j + 2 e + x; e5m2: position 16 j + 4 i + y channel 32 i + 4 j + y), fragments to registers
+        // the unit's queries into shared memory, in the MMA's channel order (fp16: position 16 j + 8 e + 2 i + x holds
+        // channel 32 i + 4 j + 2 e + x; e5m2: position 16 j + 4 i + y channel 32 i + 4 j + y)
         if (uc >= 2 && !wait_warp(q_free(uc & 1), prev2(uc))) {
           fail();
           break;
         }
-        const int rows = w.s.n * G - kTreeRows * w.rb;
-        auto row_ptr = [&](int r) {
-          const int row = kTreeRows * w.rb + r;
-          return reinterpret_cast<const uint4 *>(
-              p.q + (static_cast<long>(w.s.c0 + row / G) * p.num_q_heads + w.h * G + row % G) * kHeadDim);
-        };
-        const uint4 none = make_uint4(0, 0, 0, 0);
-        {
-          const int r = 32 * hw + lane;
-          const uint32_t qh = base + kOffQHi + (uc & 1) * kQHiBytes, q8 = base + kOffQ8 + (uc & 1) * kQ8Bytes;
-          const uint4 *src = row_ptr(r < rows ? r : 0);
-#pragma unroll 2
-          for (int t = 0; t < 4; ++t) {
-            uint4 x[4];
+        const int r = 32 * hw + lane, row = kTreeRows * w.rb + r;
+        const bool real = row < w.s.n * G;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + (static_cast<long>(w.s.c0 + (real ? row / G : 0)) * p.num_q_heads + w.h * G + (real ? row % G : 0)) * kHeadDim);
+        const uint32_t qh = base + kOffQHi + (uc & 1) * kQHiBytes, q8 = base + kOffQ8 + (uc & 1) * kQ8Bytes;
+        uint4 x[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x[c] = r < rows ? __ldg(src + 4 * c + t) : none;
-            // words of channels 32 c + 8 t ..: tiles 2t (x, y) and 2t + 1 (z, w)
-            sts128(qh + tc05::sw128_offset(r, 32 * t, kTreeRows), make_uint4(x[0].x, x[1].x, x[2].x, x[3].x));
-            sts128(qh + tc05::sw128_offset(r, 32 * t + 8, kTreeRows), make_uint4(x[0].y, x[1].y, x[2].y, x[3].y));
-            sts128(qh + tc05::sw128_offset(r, 32 * t + 16, kTreeRows), make_uint4(x[0].z, x[1].z, x[2].z, x[3].z));
-            sts128(qh + tc05::sw128_offset(r, 32 * t + 24, kTreeRows), make_uint4(x[0].w, x[1].w, x[2].w, x[3].w));
-            uint32_t lo[4], hi[4];
+        for (int c = 0; c < 16; ++c) x[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              lo[c] = e5m2x2_of_f16x2(x[c].x) | static_cast<uint32_t>(e5m2x2_of_f16x2(x[c].y)) << 16;
-              hi[c] = e5m2x2_of_f16x2(x[c].z) | static_cast<uint32_t>(e5m2x2_of_f16x2(x[c].w)) << 16;
-            }
-            sts128(q8 + tc05::sw128_offset_b8(r, 32 * t), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-            sts128(q8 + tc05::sw128_offset_b8(r, 32 * t + 16), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full(uc & 1));
+        for (int t = 0; t < 4; ++t) {
+          // words of channels 32 c + 8 t ..: tiles 2t (x, y) and 2t + 1 (z, w)
+          const uint4 &a = x[t], &b = x[4 + t], &c = x[8 + t], &d = x[12 + t];
+          sts128(qh + tc05::sw128_offset(r, 32 * t, kTreeRows), make_uint4(a.x, b.x, c.x, d.x));
+          sts128(qh + tc05::sw128_offset(r, 32 * t + 8, kTreeRows), make_uint4(a.y, b.y, c.y, d.y));
+          sts128(qh + tc05::sw128_offset(r, 32 * t + 16, kTreeRows), make_uint4(a.z, b.z, c.z, d.z));
+          sts128(qh + tc05::sw128_offset(r, 32 * t + 24, kTreeRows), make_uint4(a.w, b.w, c.w, d.w));
+          auto e5 = [](uint32_t lo, uint32_t hi) {
+            return e5m2x2_of_f16x2(lo) | static_cast<uint32_t>(e5m2x2_of_f16x2(hi)) << 16;
+          };
+          sts128(q8 + tc05::sw128_offset_b8(r, 32 * t), make_uint4(e5(a.x, a.y), e5(b.x, b.y), e5(c.x, c.y), e5(d.x, d.y)));
+          sts128(q8 + tc05::sw128_offset_b8(r, 32 * t + 16), make_uint4(e5(a.z, a.w), e5(b.z, b.w), e5(c.z, c.w), e5(d.z, d.w)));
         }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int ra = 32 * hw + 16 * m + n, rbb = ra + 8;
-          const uint4 *sa = row_ptr(ra < rows ? ra : 0) + 4 * i, *sb = row_ptr(rbb < rows ? rbb : 0) + 4 * i;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 x = ra < rows ? __ldg(sa + c) : none, y = rbb < rows ? __ldg(sb + c) : none;
-            qa[m][4 * c] = x.x; qa[m][4 * c + 1] = x.y; qa[m][4 * c + 2] = x.z; qa[m][4 * c + 3] = x.w;
-            qb[m][4 * c] = y.x; qb[m][4 * c + 1] = y.y; qb[m][4 * c + 2] = y.z; qb[m][4 * c + 3] = y.w;
-          }
-        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(uc & 1));
       }
       for (int t = w.tile; t < t1; ++t, ++kt) {
         const int x2 = kt & 1;
@@ -407,13 +412,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           }
           ++k;
           if (is_help) {
+            // rows 32 hw .. + 31 (two 16-row A tiles, by ldmatrix from the queries' shared-memory tile) times the zero
+            // points of the 8 pages (B: page n), which lie in the same channel order
             float acc[2][4] = {};
             const uint32_t z = stage + n * R::kPageStride + F::kKZero + 4 * i;
+            const uint32_t qh = base + kOffQHi + (uc & 1) * kQHiBytes;
+            const int r = 32 * hw + (lane & 15);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const uint32_t b0 = n < np ? lds32_at(z + 32 * j) : 0u, b1 = n < np ? lds32_at(z + 32 * j + 16) : 0u;
-#pragma unroll
-              for (int m = 0; m < 2; ++m) mma16816(acc[m], qa[m][2 * j], qb[m][2 * j], qa[m][2 * j + 1], qb[m][2 * j + 1], b0, b1);
+              uint32_t b0 = lds32_at(z + 32 * j), b1 = lds32_at(z + 32 * j + 16);
+              if (n >= np) b0 = b1 = 0;
+              const uint32_t qr = qh + tc05::sw128_offset(r, 16 * j + 8 * (lane >> 4), kTreeRows);
+              uint32_t a[4], c[4];
+              ldmatrix_x4<0>(qr, a[0], a[1], a[2], a[3]);
+              ldmatrix_x4<16 * 128>(qr, c[0], c[1], c[2], c[3]);
+              mma16816(acc[0], a[0], a[1], a[2], a[3], b0, b1);
+              mma16816(acc[1], c[0], c[1], c[2], c[3], b0, b1);
             }
             // shares of pages 2i, 2i + 1 for rows n, n + 8: fp16 hi at k = page, lo at k = 8 + page
             const uint32_t zo = base + kOffZero + x2 * (kTreeRows * 32);
@@ -431,44 +445,48 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             }
           } else if (is_v) {
             // pages in batches of 4; lanes 0-15 of the quarter: channels 32 wq + 4n + {0, 1}, 16-31: + {2, 3}
+            const uint32_t sv = stage + F::kVScale + 32 * i + 4 * wq, zv = stage + F::kVZero + 32 * wq + 4 * i;
+            const uint32_t cv = stage + F::kVCode + (kBits == 8 ? 512 * wq + 16 * lane
+                                                     : kBits == 4 ? 512 * (wq >> 1) + 16 * lane + 8 * (wq & 1) : 16 * lane + 4 * wq);
+            auto page = [&](int pg, uint32_t *a, uint32_t *c) {
+              const uint32_t off = pg * R::kPageStride;
+              const uint32_t s0 = lds32_at(sv + off), s1 = lds32_at(sv + off + 16), z0 = lds32_at(zv + off), z1 = lds32_at(zv + off + 16);
+              uint32_t x[4], y[4];
+              if (kBits == 8) {
+                const uint4 cw = lds128_at(cv + off);
+                tile_codes<kBits>(cw.x, cw.y, 0, x);
+                tile_codes<kBits>(cw.z, cw.w, 1, y);
+              } else if (kBits == 4) {
+                const uint2 cw = lds64_at(cv + off);
+                tile_codes<kBits>(cw.x, 0, 0, x);
+                tile_codes<kBits>(cw.y, 0, 1, y);
+              } else {
+                const uint32_t cw = lds32_at(cv + off);
+                tile_codes<kBits>(cw, 0, 0, x);
+                tile_codes<kBits>(cw, 0, 1, y);
+              }
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                if (kBits == 4) {
+                  x[r] = hmul2_u32(x[r], 0x60006000u);  // * 512: the codes
+                  y[r] = hmul2_u32(y[r], 0x60006000u);
+                }
+                a[r] = hfma2_u32(x[r], r < 2 ? s0 : s1, r < 2 ? z0 : z1);
+                c[r] = hfma2_u32(y[r], r < 2 ? s0 : s1, r < 2 ? z0 : z1);
+              }
+            };
 #pragma unroll 1
             for (int pb = 0; pb < kTilePages; pb += 4) {
               uint32_t o0[16], o1[16];
+              if (pb + 4 <= np) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t a[4] = {0, 0, 0, 0}, c[4] = {0, 0, 0, 0};
-                if (pb + j < np) {
-                  const uint32_t blk = stage + (pb + j) * R::kPageStride;
-                  const uint32_t s0 = lds32_at(blk + F::kVScale + 32 * i + 4 * wq), s1 = lds32_at(blk + F::kVScale + 32 * i + 16 + 4 * wq);
-                  const uint32_t z0 = lds32_at(blk + F::kVZero + 32 * wq + 4 * i), z1 = lds32_at(blk + F::kVZero + 32 * wq + 4 * i + 16);
-                  if (kBits == 8) {
-                    const uint4 cw = lds128_at(blk + F::kVCode + 512 * wq + 16 * lane);
-                    tile_codes<kBits>(cw.x, cw.y, 0, a);
-                    tile_codes<kBits>(cw.z, cw.w, 1, c);
-                  } else if (kBits == 4) {
-                    const uint2 cw = lds64_at(blk + F::kVCode + 512 * (wq >> 1) + 16 * lane + 8 * (wq & 1));
-                    tile_codes<kBits>(cw.x, 0, 0, a);
-                    tile_codes<kBits>(cw.y, 0, 1, c);
-                  } else {
-                    const uint32_t cw = lds32_at(blk + F::kVCode + 16 * lane + 4 * wq);
-                    tile_codes<kBits>(cw, 0, 0, a);
-                    tile_codes<kBits>(cw, 0, 1, c);
-                  }
+                for (int j = 0; j < 4; ++j) page(pb + j, o0 + 4 * j, o1 + 4 * j);
+              } else {  // missing pages are zeros: their weights are 0, and 0 * what the stage held need not be
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) {
-                    if (kBits == 4) {
-                      a[r] = hmul2_u32(a[r], 0x60006000u);  // * 512: the codes
-                      c[r] = hmul2_u32(c[r], 0x60006000u);
-                    }
-                    a[r] = hfma2_u32(a[r], r < 2 ? s0 : s1, r < 2 ? z0 : z1);
-                    c[r] = hfma2_u32(c[r], r < 2 ? s0 : s1, r < 2 ? z0 : z1);
-                  }
-                }
+                for (int j = 0; j < 16; ++j) o0[j] = o1[j] = 0;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  o0[4 * j + r] = a[r];
-                  o1[4 * j + r] = c[r];
-                }
+                for (int j = 0; j < 4; ++j)
+                  if (pb + j < np) page(pb + j, o0 + 4 * j, o1 + 4 * j);
               }
               tc05::tmem_st_frag16(tV + lane_base + 8 * pb, o0);
               tc05::tmem_st_frag16(tV + lane_base + (16u << 16) + 8 * pb, o1);
@@ -505,7 +523,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
                   const uint32_t c4 = hmul2_u32(a[r], quarter_unit<kBits>()), sr = s[2 * q + (r >> 1)];
                   const uint32_t hr = hmul2_u32(c4, sr);
                   hi[4 * q + r] = hr;
-                  l8[r] = e5m2x2_of_f16x2(hfma2_u32(c4, sr, hneg2_u32(hr)));  // the exact remainder, rounded to e5m2
+                  l8[r] = e5m2x2_of_f16x2(h2_as_u32(__hfma2(u32_as_h2(c4), u32_as_h2(sr), __hneg2(u32_as_h2(hr)))));  // the exact remainder, rounded to e5m2
                 }
                 lo[2 * q] = l8[0] | static_cast<uint32_t>(l8[2]) << 16;
                 lo[2 * q + 1] = l8[1] | static_cast<uint32_t>(l8[3]) << 16;
@@ -561,25 +579,33 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             }
           } else {
 #pragma unroll 1
-            for (int ph = 0; ph < 4; ++ph) {
-              const int grp = 2 * wq + (ph >> 1), hf = ph & 1;
+            for (int e = 0; e < 2; ++e) {
               int count;
               long stride;
-              const __half *rk = rows_of(grp, p.k, p.res_k, count, stride) + 32 * i + 16 * hf;
-              uint32_t hi[16];
+              const __half *rk = rows_of(2 * wq + e, p.k, p.res_k, count, stride) + 32 * i;
+              if (count <= 0) break;  // and none in the groups behind it but the residual's, which is no odd one
+              uint4 x[4], y[4];
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                if (n < count) x = *reinterpret_cast<const uint4 *>(rk + n * stride + 8 * c);
-                if (n + 8 < count) y = *reinterpret_cast<const uint4 *>(rk + (n + 8) * stride + 8 * c);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {  // in quarters, as the quantized keys
-                  hi[8 * c + 2 * e] = hmul2_u32(xs[e], 0x34003400u);
-                  hi[8 * c + 2 * e + 1] = hmul2_u32(ys[e], 0x34003400u);
-                }
+              for (int c = 0; c < 4; ++c) {
+                x[c] = y[c] = make_uint4(0, 0, 0, 0);
+                if (n < count) x[c] = *reinterpret_cast<const uint4 *>(rk + n * stride + 8 * c);
+                if (n + 8 < count) y[c] = *reinterpret_cast<const uint4 *>(rk + (n + 8) * stride + 8 * c);
               }
-              tc05::tmem_st_frag16(tKhi + lane_base + (static_cast<uint32_t>(16 * (ph >> 1)) << 16) + 32 * hf, hi);
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                uint32_t hi[16];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const uint4 &u = x[2 * hf + c], &v = y[2 * hf + c];
+                  const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {  // in quarters, as the quantized keys
+                    hi[8 * c + 2 * q] = hmul2_u32(us[q], 0x34003400u);
+                    hi[8 * c + 2 * q + 1] = hmul2_u32(vs[q], 0x34003400u);
+                  }
+                }
+                tc05::tmem_st_frag16(tKhi + lane_base + (static_cast<uint32_t>(16 * e) << 16) + 32 * hf, hi);
+              }
             }
           }
         }
@@ -669,9 +695,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       float l[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) l[j] = 0.f;
-      float myref = -INFINITY;  // lane j: the reference of row j (every warp of the group holds the same)
+      float myref = 0.f;  // lane j: the reference of row j (every warp of the group holds the same)
       if (rows > 0) {
-        if (wq == 0) reinterpret_cast<float *>(sm + kOffRef)[32 * g + lane] = INFINITY;
+        if (wq == 0) reinterpret_cast<float *>(sm + kOffRef)[32 * g + lane] = 0.f;
         group_sync(bid);
       }
       uint32_t seen = 0;  // tile 0: the rows that see this token
@@ -730,9 +756,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           continue;
         }
         tc05::fence_after_sync();
-        uint32_t sv[32];
+        float sv[32];
         auto load = [&]() {
-          tc05::tmem_ld32(tmem + kTmS + 64u * x2 + 32u * g + lane_base, sv);
+          tc05::tmem_ld32(tmem + kTmS + 64u * x2 + 32u * g + lane_base, reinterpret_cast<uint32_t (&)[32]>(sv));
           tc05::tmem_wait_ld();
         };
         // logits in log2 units minus the reference; -inf where this token is not seen
@@ -742,8 +768,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const uint4 r = lds128_at(s_ref + 4 * j);
-            float2 a = make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
-            float2 b = make_float2(__uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3]));
+            float2 a = make_float2(sv[j], sv[j + 1]), b = make_float2(sv[j + 2], sv[j + 3]);
             a = fma2(a, make_float2(sc, sc), make_float2(__uint_as_float(r.x), __uint_as_float(r.y)));
             b = fma2(b, make_float2(sc, sc), make_float2(__uint_as_float(r.z), __uint_as_float(r.w)));
             if (mask != 0xFFFFFFFFu) {
@@ -754,35 +779,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             }
             m0 = fmax3(m0, a.x, a.y);
             m1 = fmax3(m1, b.x, b.y);
-            sv[j] = __float_as_uint(a.x);
-            sv[j + 1] = __float_as_uint(a.y);
-            sv[j + 2] = __float_as_uint(b.x);
-            sv[j + 3] = __float_as_uint(b.y);
+            sv[j] = a.x;
+            sv[j + 1] = a.y;
+            sv[j + 2] = b.x;
+            sv[j + 3] = b.y;
           }
           return fmaxf(m0, m1);
         };
         load();
         const float top = shift();
-        if (group_any(bid, top > kRefSlack || !ok)) {
+        if (group_any(bid, top > kRefSlack || t == t0 || !ok)) {
           if (group_any(bid, !ok)) {
             fail();
             break;
           }
-          // move references: the tile's maximum of each row, lane j keeps row j's
-          load();
-          float mine = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float m = redux_max(mask >> j & 1 ? __uint_as_float(sv[j]) * sc : -INFINITY);
-            if (lane == j) mine = m;
-          }
-          red[32 * wq + lane] = mine;
+          // move references: lane j finds the tile's maximum of row j
+          red[32 * wq + lane] = warp_reduce_rows(sv, lane, [](float a, float b) { return fmaxf(a, b); });
           group_sync(bid);
-          mine = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));
-          const float now = mine > myref + kRefSlack ? mine : myref;
-          const float f = now == myref ? 1.0f : fast_exp2(myref - now);  // 0 where there was no reference yet
-          myref = now;
-          if (wq == 0) reinterpret_cast<float *>(sm + kOffRef)[32 * g + lane] = -now;
+          const float up = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));
+          const float by = (t == t0 || up > kRefSlack) ? up : 0.f;
+          const float f = fast_exp2(-by);
+          myref += by;
+          if (wq == 0) reinterpret_cast<float *>(sm + kOffRef)[32 * g + lane] = -myref;
           group_sync(bid);
           if (t > t0) {
             // the sums so far, and O once every product before this tile's is in it
@@ -815,9 +833,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = 8 * c + 2 * e;
-            const float2 x = make_float2(fast_exp2(__uint_as_float(sv[j])), fast_exp2(__uint_as_float(sv[j + 1])));
-            l[j] += x.x;
-            l[j + 1] += x.y;
+            const float2 x = make_float2(fast_exp2(sv[j]), fast_exp2(sv[j + 1]));
+            const float2 ls = add2(make_float2(l[j], l[j + 1]), x);
+            l[j] = ls.x;
+            l[j + 1] = ls.y;
             const __half2 hh = __floats2half2_rn(x.x, x.y);
             const float2 d = sub2(x, __half22float2(hh));
             hi[e] = h2_as_u32(hh);
@@ -835,16 +854,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 
       // ---- the piece's end: sums over the tokens (lane j: row j), O once its last product is in it
       if (rows > 0) {
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) {
-#pragma unroll
-          for (int j = 0; j < s; ++j) {
-            const bool up = lane & s;
-            const float keep = up ? l[j + s] : l[j], send = up ? l[j] : l[j + s];
-            l[j] = keep + __shfl_xor_sync(kAll, send, s);
-          }
-        }
-        red[32 * wq + lane] = l[0];
+        red[32 * wq + lane] = warp_reduce_rows(l, lane, [](float a, float b) { return a + b; });
         ok = ok && wait_warp(p_free((kt - 1) & 1), ((kt - 1) >> 1) & 1);
         if (group_any(bid, !ok)) {
           fail();
@@ -852,31 +862,39 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         }
         const float lsum = red[lane] + red[32 + lane] + red[64 + lane] + red[96 + lane];
         tc05::fence_after_sync();
-        uint32_t o[32];
-        tc05::tmem_ld32(tO, o);
+        float o[32];
+        tc05::tmem_ld32(tO, reinterpret_cast<uint32_t (&)[32]>(o));
         tc05::tmem_wait_ld();
         const int row0 = kTreeRows * w.rb + kGroupRows * g;
         const int ch = 32 * wq + 4 * (lane & 7) + 2 * (lane >> 4) + (lane >> 3 & 1);  // the channel of this lane
-        auto out_ptr = [&](int row) {
-          return p.out + (static_cast<long>(w.s.c0 + row / G) * p.num_q_heads + w.h * G + row % G) * kHeadDim + ch;
-        };
-        if (t0 == 0 && t1 == w.s.tiles) {
-          const float inv = 1.0f / lsum;
+        // out of row j = o[j] times lane j's factor
+        auto store = [&](float factor) {
+          int head = row0 % G;
+          __half *dst = p.out + (static_cast<long>(w.s.c0 + row0 / G) * p.num_q_heads + w.h * G + head) * kHeadDim + ch;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const float ij = __shfl_sync(kAll, inv, j);
-            if (j < rows) *out_ptr(row0 + j) = __float2half_rn(__uint_as_float(o[j]) * ij);
+            const __half x = __float2half_rn(o[j] * __shfl_sync(kAll, factor, j));
+            if (j < rows) *dst = x;
+            dst += kHeadDim;
+            if (++head == G) {
+              head = 0;
+              dst += static_cast<long>(p.num_q_heads - G) * kHeadDim;
+            }
           }
+        };
+        if (t0 == 0 && t1 == w.s.tiles) {
+          store(1.0f / lsum);
         } else {
           const long long slot = 2ll * blockIdx.x + (first_piece ? 0 : 1);
           float *dst = p.part + (slot * kTreeRows + kGroupRows * g) * kHeadDim + ch;
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (j < rows) dst[j * kHeadDim] = __uint_as_float(o[j]);
+            if (j < rows) dst[j * kHeadDim] = o[j];
           if (wq == 0) p.part_ml[slot * kTreeRows + kGroupRows * g + lane] = make_float2(myref, lsum);
           __threadfence();
           group_sync(bid);
-          const long long wf = cta_of(w.start, T, W), wl = cta_of(w.start + w.s.tiles - 1, T, W);
+          const TreeSplit split = *reinterpret_cast<const TreeSplit *>(sm + kOffSplit);
+          const int wf = split.cta_of(w.start), wl = split.cta_of(w.start + w.s.tiles - 1);
           const int rbs = (p.max_nodes * G + kTreeRows - 1) / kTreeRows;
           uint32_t *ticket = p.tickets + ((static_cast<long>(w.b) * H + w.h) * rbs + w.rb) * 2 + g;
           if (wq == 0 && lane == 0) {
@@ -886,25 +904,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           }
           group_sync(bid);
           if (*last_flag) {
-            // merge the unit's pieces in their order; this thread owns a channel
+            // merge the unit's pieces in their order: lane j the sums of row j, every thread its channel of all rows
             __threadfence();
-            auto slot_of = [&](long long c) { return 2 * c + ((c == wf && c * T / W < w.start) ? 1 : 0); };
-            for (int j = 0; j < rows; ++j) {
-              float M = -INFINITY;
-              for (long long c = wf + lane; c <= wl; c += 32)
-                M = fmaxf(M, __ldcg(p.part_ml + slot_of(c) * kTreeRows + kGroupRows * g + j).x);
-              M = redux_max(M);
-              float acc = 0.f, sum = 0.f;
+            const int odd = split.first(wf) < w.start;  // the unit is the last of its first CTA's pieces
+            auto slot_of = [&](int c) { return (2ll * c + (c == wf ? odd : 0)) * kTreeRows + kGroupRows * g; };
+            float M = -INFINITY, sum = 0.f;
 #pragma unroll 4
-              for (long long c = wf; c <= wl; ++c) {
-                const long long at = slot_of(c) * kTreeRows + kGroupRows * g + j;
-                const float2 ml = __ldcg(p.part_ml + at);
-                const float wt = fast_exp2(ml.x - M);
-                sum += wt * ml.y;
-                acc += wt * __ldcg(p.part + at * kHeadDim + ch);
-              }
-              *out_ptr(row0 + j) = __float2half_rn(acc / sum);
+            for (int c = wf; c <= wl; ++c) M = fmaxf(M, __ldcg(p.part_ml + slot_of(c) + lane).x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0.f;
+#pragma unroll 1
+            for (int c = wf; c <= wl; ++c) {
+              const long long at = slot_of(c);
+              const float *src = p.part + at * kHeadDim + ch;
+              float v[32];  // rows that the unit does not have hold anything and are not stored
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __ldcg(src + j * kHeadDim);
+              const float2 ml = __ldcg(p.part_ml + at + lane);
+              const float wt = fast_exp2(ml.x - M);
+              sum += wt * ml.y;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] += __shfl_sync(kAll, wt, j) * v[j];
             }
+            store(1.0f / sum);
           }
           group_sync(bid);  // the flag is read before another piece sets it
         }
