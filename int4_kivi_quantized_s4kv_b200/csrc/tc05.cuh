@@ -70,12 +70,14 @@ __host__ __device__ __forceinline__ uint32_t plain16_offset(int r, int k) {
   return static_cast<uint32_t>((r >> 3) * 256 + (k >> 3) * 128 + (r & 7) * 16 + (k & 7) * 2);
 }
 
-// Descriptor of a 64-column fp16 operand that lies k-row by k-row (its 64 columns
-// contiguous, "MN-major") with the 128-byte swizzle: 8 rows make an atom of 1024
-// bytes, in which the 16-byte chunk c of row k sits at position c ^ (k % 8).
-__device__ __forceinline__ uint64_t smem_desc_mn64(uint32_t addr) {
+// Descriptor of an fp16 operand that lies k-row by k-row (64 columns contiguous,
+// "MN-major") with the 128-byte swizzle: 8 rows of 64 columns make an atom of 1024
+// bytes, in which the 16-byte chunk c of row k sits at position c ^ (k % 8); the next 8
+// rows follow it (stride 1024), the next 64 columns lie `cols_stride` bytes away (the
+// leading-byte offset).
+__device__ __forceinline__ uint64_t smem_desc_mn64(uint32_t addr, uint32_t cols_stride) {
   uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(1024 >> 4) << 16;
+  d |= static_cast<uint64_t>(cols_stride >> 4) << 16;
   d |= static_cast<uint64_t>(1024 >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;

@@ -23,7 +23,7 @@
 // fragment's registers down as they come, so unpacking a page is the same
 // straight-line code as in decode attention and no dequantized byte goes through
 // shared memory.  Keys: S = sum q (code scale) + sum q zero.  code/4 * scale is kept as
-// its fp16 rounding and the exact remainder, rounded to e5m2 (a second, fp8 MMA
+// its fp16 rounding and the exact remainder, cut to e5m2 (a second, fp8 MMA
 // against an e5m2 copy of q): the factor 1/4 keeps any fp16 range finite, and a
 // key is carried to about 2^-14 of code * scale, as in prefill attention.  The zero
 // points' share is one number a (page, row): two helper warps compute it with
@@ -61,10 +61,10 @@ constexpr float kZeroUnit = 0x1p-10f;      // zero-point shares enter as share *
 
 constexpr uint32_t kIdescTS = tc05::idesc_f16_f32(128, kTreeRows);
 constexpr uint32_t kIdescTS8 = tc05::idesc_e5m2_f32(128, kTreeRows);
-constexpr uint32_t kIdescTO = tc05::idesc_f16_f32(128, kTreeRows) | tc05::kIdescMnB;
+constexpr uint32_t kIdescTO = tc05::idesc_f16_f32(128, 2 * kTreeRows) | tc05::kIdescMnB;  // weights hi | lo
 
-// tensor memory, all 512 columns: S [2], O, K hi [2], V [2], K lo [2]
-constexpr uint32_t kTmS = 0, kTmO = 128, kTmKhi = 192, kTmV = 320, kTmKlo = 448;
+// tensor memory, all 512 columns: S, O (hi | lo), K hi [2], V [2], K lo [2]
+constexpr uint32_t kTmS = 0, kTmO = 64, kTmKhi = 192, kTmV = 320, kTmKlo = 448;
 
 // shared memory
 constexpr uint32_t kQHiBytes = kTreeRows * 256, kQ8Bytes = kTreeRows * 128, kPBytes = kTile * kTreeRows * 2;
@@ -214,8 +214,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   auto k_free = [&](int x) { return bar(14 + x); };
   auto v_ready = [&](int x) { return bar(16 + x); };
   auto v_free = [&](int x) { return bar(18 + x); };
-  auto s_full = [&](int x) { return bar(20 + x); };
-  auto s_free = [&](int x) { return bar(22 + x); };
+  const uint32_t s_full = bar(20), s_free = bar(22);
   auto p_full = [&](int x) { return bar(24 + x); };
   auto p_free = [&](int x) { return bar(26 + x); };
   auto q_full = [&](int x) { return bar(28 + x); };
@@ -288,13 +287,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       mbar_init(k_free(x), 1);
       mbar_init(v_ready(x), 4);
       mbar_init(v_free(x), 1);
-      mbar_init(s_full(x), 1);
-      mbar_init(s_free(x), 8);
       mbar_init(p_full(x), 8);
       mbar_init(p_free(x), 1);
       mbar_init(q_full(x), 2);
       mbar_init(q_free(x), 1);
     }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 8);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -517,16 +516,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
               for (int q = 0; q < 4; ++q) {
                 uint32_t a[4];
                 tile_codes<kBits>(kBits == 8 ? cw[2 * q] : kBits == 4 ? cw[q] : cw[q >> 1], kBits == 8 ? cw[2 * q + 1] : 0, q & 1, a);
-                uint16_t l8[4];
+                uint32_t rem[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                   const uint32_t c4 = hmul2_u32(a[r], quarter_unit<kBits>()), sr = s[2 * q + (r >> 1)];
                   const uint32_t hr = hmul2_u32(c4, sr);
                   hi[4 * q + r] = hr;
-                  l8[r] = e5m2x2_of_f16x2(h2_as_u32(__hfma2(u32_as_h2(c4), u32_as_h2(sr), __hneg2(u32_as_h2(hr)))));  // the exact remainder, rounded to e5m2
+                  rem[r] = h2_as_u32(__hfma2(u32_as_h2(c4), u32_as_h2(sr), __hneg2(u32_as_h2(hr))));  // exact
                 }
-                lo[2 * q] = l8[0] | static_cast<uint32_t>(l8[2]) << 16;
-                lo[2 * q + 1] = l8[1] | static_cast<uint32_t>(l8[3]) << 16;
+                // an fp16 number's upper byte is its e5m2 truncation (3 significant bits of the remainder)
+                lo[2 * q] = __byte_perm(rem[0], rem[2], 0x7531);
+                lo[2 * q + 1] = __byte_perm(rem[1], rem[3], 0x7531);
               }
               const uint32_t at = lane_base + (static_cast<uint32_t>(16 * (ph >> 1)) << 16);
               tc05::tmem_st_frag16(tKhi + at + 32 * hf, hi);
@@ -630,14 +630,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       const int x2 = k1 & 1;
       if (!wait_warp(v_ready(x2), (k1 >> 1) & 1) || !wait_warp(p_full(x2), (k1 >> 1) & 1)) return false;
       tc05::fence_after_sync();
-      const uint64_t dhi = tc05::smem_desc_mn64(base + kOffP + (2 * x2) * kPBytes);
-      const uint64_t dlo = tc05::smem_desc_mn64(base + kOffP + (2 * x2 + 1) * kPBytes);
+      const uint64_t dp = tc05::smem_desc_mn64(base + kOffP + (2 * x2) * kPBytes, kPBytes);
       const uint32_t tV = tmem + kTmV + 64u * x2;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        tc05::mma_f16_ts(tmem + kTmO, tV + 8 * j, dhi + ((2048 * j) >> 4), kIdescTO, (!fresh || j > 0) ? 1u : 0u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) tc05::mma_f16_ts(tmem + kTmO, tV + 8 * j, dlo + ((2048 * j) >> 4), kIdescTO, 1u);
+        tc05::mma_f16_ts(tmem + kTmO, tV + 8 * j, dp + ((2048 * j) >> 4), kIdescTO, (!fresh || j > 0) ? 1u : 0u);
       tc05::mma_commit(p_free(x2));
       tc05::mma_commit(v_free(x2));
       return true;
@@ -649,12 +646,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       for (int t = w.tile; t < t1; ++t, ++kt) {
         const int x2 = kt & 1;
         if ((t == w.tile && !wait_warp(q_full(uc & 1), (uc >> 1) & 1)) || !wait_warp(k_ready(x2), (kt >> 1) & 1) ||
-            (kt >= 2 && !wait_warp(s_free(x2), prev2(kt)))) {
+            (kt >= 1 && !wait_warp(s_free, (kt - 1) & 1))) {
           fail();
           break;
         }
         tc05::fence_after_sync();
-        const uint32_t tS = tmem + kTmS + 64u * x2, tKhi = tmem + kTmKhi + 64u * x2, tKlo = tmem + kTmKlo + 32u * x2;
+        const uint32_t tS = tmem + kTmS, tKhi = tmem + kTmKhi + 64u * x2, tKlo = tmem + kTmKlo + 32u * x2;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           tc05::mma_f16_ts(tS, tKhi + 8 * j, dq + (((j >> 2) * (kQHiBytes / 2) + (j & 3) * 32) >> 4), kIdescTS, j > 0 ? 1u : 0u);
@@ -663,7 +660,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           for (int j = 0; j < 4; ++j) tc05::mma_e5m2_ts(tS, tKlo + 8 * j, dq8 + ((32 * j) >> 4), kIdescTS8, 1u);
           tc05::mma_f16_ss(tS, dhot, tc05::smem_desc_plain16(base + kOffZero + x2 * (kTreeRows * 32)), kIdescTS, 1u);
         }
-        tc05::mma_commit(s_full(x2));
+        tc05::mma_commit(s_full);
         tc05::mma_commit(k_free(x2));
         if (t + 1 == t1) tc05::mma_commit(q_free(uc & 1));
         if (kt > 0 && !issue_pv(kt - 1)) {
@@ -742,7 +739,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       }
       for (int t = t0; t < t1; ++t, ++kt) {
         const int x2 = kt & 1;
-        ok = ok && wait_warp(s_full(x2), (kt >> 1) & 1);
+        ok = ok && wait_warp(s_full, kt & 1);
         if (rows <= 0) {  // nothing to do but to keep the barriers' counts
           ok = ok && (kt < 2 || wait_warp(p_free(x2), prev2(kt)));
           if (!ok) {
@@ -750,7 +747,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             break;
           }
           if (lane == 0) {
-            mbar_arrive(s_free(x2));
+            mbar_arrive(s_free);
             mbar_arrive(p_full(x2));
           }
           continue;
@@ -758,11 +755,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         tc05::fence_after_sync();
         float sv[32];
         auto load = [&]() {
-          tc05::tmem_ld32(tmem + kTmS + 64u * x2 + 32u * g + lane_base, reinterpret_cast<uint32_t (&)[32]>(sv));
+          tc05::tmem_ld32(tmem + kTmS + 32u * g + lane_base, reinterpret_cast<uint32_t (&)[32]>(sv));
           tc05::tmem_wait_ld();
         };
         // logits in log2 units minus the reference; -inf where this token is not seen
         const uint32_t mask = t == 0 ? seen : (tl / kPage < w.pages(t) ? 0xFFFFFFFFu : 0u);
+        const bool masked = __any_sync(kAll, mask != 0xFFFFFFFFu);
         auto shift = [&]() {
           float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
@@ -771,7 +769,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             float2 a = make_float2(sv[j], sv[j + 1]), b = make_float2(sv[j + 2], sv[j + 3]);
             a = fma2(a, make_float2(sc, sc), make_float2(__uint_as_float(r.x), __uint_as_float(r.y)));
             b = fma2(b, make_float2(sc, sc), make_float2(__uint_as_float(r.z), __uint_as_float(r.w)));
-            if (mask != 0xFFFFFFFFu) {
+            if (masked) {
               a.x = mask >> j & 1 ? a.x : -INFINITY;
               a.y = mask >> (j + 1) & 1 ? a.y : -INFINITY;
               b.x = mask >> (j + 2) & 1 ? b.x : -INFINITY;
@@ -806,16 +804,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             // the sums so far, and O once every product before this tile's is in it
             ok = ok && wait_warp(p_free(x2 ^ 1), ((kt - 1) >> 1) & 1);
             tc05::fence_after_sync();
-            uint32_t o[32];
-            tc05::tmem_ld32(tO, o);
-            tc05::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float fj = __shfl_sync(kAll, f, j);
-              l[j] *= fj;
-              o[j] = __float_as_uint(__uint_as_float(o[j]) * fj);
+            for (int j = 0; j < 32; ++j) l[j] *= __shfl_sync(kAll, f, j);
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+              uint32_t o[32];
+              tc05::tmem_ld32(tO + kTreeRows * part, o);
+              tc05::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * __shfl_sync(kAll, f, j));
+              tc05::tmem_st32(tO + kTreeRows * part, o);
             }
-            tc05::tmem_st32(tO, o);
             tc05::tmem_wait_st();
           }
           load();
@@ -824,7 +823,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         // S has been read
         tc05::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_free(x2));
+        if (lane == 0) mbar_arrive(s_free);
         ok = ok && (kt < 2 || wait_warp(p_free(x2), prev2(kt)));
         const uint32_t ph = base + kOffP + (2 * x2) * kPBytes + (tl >> 3) * 1024 + (tl & 7) * 128;
 #pragma unroll
@@ -863,8 +862,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         const float lsum = red[lane] + red[32 + lane] + red[64 + lane] + red[96 + lane];
         tc05::fence_after_sync();
         float o[32];
-        tc05::tmem_ld32(tO, reinterpret_cast<uint32_t (&)[32]>(o));
-        tc05::tmem_wait_ld();
+        {
+          float lo[32];
+          tc05::tmem_ld32(tO, reinterpret_cast<uint32_t (&)[32]>(o));
+          tc05::tmem_ld32(tO + kTreeRows, reinterpret_cast<uint32_t (&)[32]>(lo));
+          tc05::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] += lo[j];
+        }
         const int row0 = kTreeRows * w.rb + kGroupRows * g;
         const int ch = 32 * wq + 4 * (lane & 7) + 2 * (lane >> 4) + (lane >> 3 & 1);  // the channel of this lane
         // out of row j = o[j] times lane j's factor
