@@ -461,10 +461,10 @@ __device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity) {
   }
 }
 
-// The same with the waiting warp suspended by the barrier unit, up to a few
-// microseconds a try: a spinning warp would take issue slots from those at work.
-__device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, const volatile int *abort) {
-  if (mbar_try_wait(bar, parity)) return true;
+// The same for a whole warp, kept short where the phase is complete already (the
+// usual case): the loop lies out of line, and its tries suspend the warp for up to a few
+// microseconds, so that it takes no issue slots from those at work.
+static __device__ __noinline__ bool wait_warp_slow(uint32_t bar, uint32_t parity, const volatile int *abort) {
   const long long t0 = clock64();
   while (true) {
     uint32_t done;
@@ -475,9 +475,13 @@ __device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, co
         : "=r"(done)
         : "r"(bar), "r"(parity), "r"(4000)
         : "memory");
-    if (done) return true;
-    if (*abort || clock64() - t0 > kAbortWaitCycles) return false;
+    if (__all_sync(0xFFFFFFFFu, done)) return true;
+    if (__any_sync(0xFFFFFFFFu, *abort || clock64() - t0 > kAbortWaitCycles)) return false;
   }
+}
+__device__ __forceinline__ bool wait_warp_abort(uint32_t bar, uint32_t parity, const volatile int *abort) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return wait_warp_slow(bar, parity, abort);
 }
 
 }  // namespace s4kv

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     failed = true;
     *abort_flag = 1;
   };
-  auto wait_warp = [&](uint32_t b_, uint32_t parity) { return __all_sync(kAll, wait_suspended(b_, parity, abort_flag)); };
+  auto wait_warp = [&](uint32_t b_, uint32_t parity) { return wait_warp_abort(b_, parity, abort_flag); };
   // the phase of the use before the one of count k, of two buffers in turn
   auto prev2 = [](int k) { return static_cast<uint32_t>(((k >> 1) - 1) & 1); };
 
