@@ -471,6 +471,7 @@ S4KV_API int s4kv_tree_attention(const s4kv_cache_t *cache, const void *q, const
  *  tokens, parents  device int32 [n_nodes]; cu_nodes device int32 [batch+1].
  *          A token outside [0, vocab) sets S4KV_EFLAG_TREE and is passed over;
  *          a node with a parent outside [0, own index) is no node's child.
+ *  vocab   at most 2^30.
  *  target_probs  device [n_nodes] rows of vocab entries, row i at element
  *          i * target_stride: what the target gives to follow node i, summing
  *          to 1.  draft_probs the same for the draft, or NULL.

@@ -102,7 +102,7 @@ def _check(status: int, what: str):
 def _stream(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -347,31 +347,38 @@ def s4kv_swap_in(cache: S4KVCache, pages, staging, host_src, stream=None):
 # (all on one), whichever device is current, and by default on that device's
 # current stream.
 
-def _device(lead, *tensors):
-    """The one CUDA device of all these tensors."""
-    dev = lead.device
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got {dev}")
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got {t.device}")
-    return dev
+# Their kernels take a few microseconds, so the checks are kept as short as
+# they can be: one helper call an argument.
+
+def _arg(t, dtype, shape, dev, name):
+    """The address of a contiguous tensor of this type and shape on CUDA device `dev`."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: all tensors must be on CUDA device {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-
-
-def _call(dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` current."""
+def _call(what, dev, stream, fn, *args):
+    """fn(*args, stream) with device `dev` current; a status other than OK raises."""
     import torch
+    if dev < 0:
+        raise ValueError(f"{what}: expected CUDA tensors")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
-    with torch.cuda.device(dev):
-        return fn(*args, _stream(stream))
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, int(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, int(stream))
+    if status:
+        raise S4KVError(status, what)
 
 
 def s4kv_tree_workspace_size(num_q_heads: int, num_kv_heads: int, batch: int, max_nodes_per_seq: int) -> int:
@@ -397,26 +404,18 @@ def s4kv_tree_attention(cache: S4KVCache, q, k, v, cu_nodes, parents, seq_lens, 
     owns the nodes cu_nodes[b] .. cu_nodes[b+1]-1; parents int32 [n_nodes] are
     indices inside the sequence, -1 for a child of the last cached token."""
     import torch
-    if sm_scale is None:
-        sm_scale = HEAD_DIM ** -0.5
-    n_nodes, num_q_heads, _ = q.shape
+    n_nodes, num_q_heads = q.shape[0], q.shape[1]
     batch, max_pages = block_tables.shape
     kv = (n_nodes, cache.num_kv_heads, HEAD_DIM)
-    _shape(q, (n_nodes, num_q_heads, HEAD_DIM), "q")
-    _shape(k, kv, "k")
-    _shape(v, kv, "v")
-    _shape(out, tuple(q.shape), "out")
-    _shape(cu_nodes, (batch + 1,), "cu_nodes")
-    _shape(parents, (n_nodes,), "parents")
-    _shape(seq_lens, (batch,), "seq_lens")
-    dev = _device(cache.pool, q, k, v, out, cu_nodes, parents, seq_lens, block_tables, workspace)
-    f16, i32 = torch.float16, torch.int32
-    _check(_call(dev, stream, lib().s4kv_tree_attention, cache.ref, _ptr(q, f16, "q"), _ptr(k, f16, "k"),
-                 _ptr(v, f16, "v"), num_q_heads, n_nodes, _ptr(cu_nodes, i32, "cu_nodes"),
-                 _ptr(parents, i32, "parents"), _ptr(seq_lens, i32, "seq_lens"),
-                 _ptr(block_tables, i32, "block_tables"), batch, max_pages, int(max_nodes_per_seq), float(sm_scale),
-                 _ptr(out, f16, "out"), _ptr(workspace, torch.uint8, "workspace"), workspace.numel()),
-           "s4kv_tree_attention")
+    rows = (n_nodes, num_q_heads, HEAD_DIM)
+    f16, i32, dev = torch.float16, torch.int32, cache.pool.get_device()
+    _call("s4kv_tree_attention", dev, stream, lib().s4kv_tree_attention, cache.ref, _arg(q, f16, rows, dev, "q"),
+          _arg(k, f16, kv, dev, "k"), _arg(v, f16, kv, dev, "v"), num_q_heads, n_nodes,
+          _arg(cu_nodes, i32, (batch + 1,), dev, "cu_nodes"), _arg(parents, i32, (n_nodes,), dev, "parents"),
+          _arg(seq_lens, i32, (batch,), dev, "seq_lens"),
+          _arg(block_tables, i32, (batch, max_pages), dev, "block_tables"), batch, max_pages, max_nodes_per_seq,
+          HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, _arg(out, f16, rows, dev, "out"),
+          _arg(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel())
 
 
 def s4kv_verify_tree(tokens, parents, cu_nodes, target_probs, draft_probs, uniforms, path, path_len, next_token,
@@ -428,36 +427,35 @@ def s4kv_verify_tree(tokens, parents, cu_nodes, target_probs, draft_probs, unifo
     or None for proposals chosen without randomness.  Fills path int32
     [batch][max_nodes], path_len and next_token int32 [batch]."""
     import torch
-    types = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
     n_nodes, vocab = target_probs.shape
     batch, max_nodes = path.shape
-    for name, rows in (("target_probs", target_probs), ("draft_probs", draft_probs)):
-        if rows is None:
-            continue
-        if rows.dtype not in types or rows.dtype != target_probs.dtype:
-            raise TypeError(f"{name}: expected float32, float16 or bfloat16 (one type), got {rows.dtype}")
-        _shape(rows, (n_nodes, vocab), name)
-        if rows.numel() and rows.stride(1) != 1 and vocab > 1:
+    i32, dev = torch.int32, target_probs.get_device()
+    kind = target_probs.dtype
+    types = (torch.float32, torch.float16, torch.bfloat16)
+    if kind not in types:
+        raise TypeError(f"target_probs: expected float32, float16 or bfloat16, got {kind}")
+
+    def rows_of(t, name):  # address and stride; a single row has no stride of its own
+        if t.dtype is not kind:
+            raise TypeError(f"{name}: expected {kind}, the type of target_probs, got {t.dtype}")
+        if t.shape != target_probs.shape:
+            raise ValueError(f"{name}: expected shape {(n_nodes, vocab)}, got {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: all tensors must be on CUDA device {dev}, got {t.device}")
+        row, one = t.stride()
+        if one != 1 and vocab > 1 and n_nodes > 0:
             raise ValueError(f"{name}: the entries of a row must be contiguous")
-    for name, t, shape in (("tokens", tokens, (n_nodes,)), ("parents", parents, (n_nodes,)),
-                           ("cu_nodes", cu_nodes, (batch + 1,)), ("uniforms", uniforms, (n_nodes,)),
-                           ("path_len", path_len, (batch,)), ("next_token", next_token, (batch,))):
-        _shape(t, shape, name)
-    dev = _device(target_probs, draft_probs, tokens, parents, cu_nodes, uniforms, path, path_len, next_token, err_flag)
-    i32 = torch.int32
+        return t.data_ptr(), row if n_nodes > 1 else vocab
 
-    def rows_of(t):  # address and stride; one row has no stride of its own
-        if t is None:
-            return None, 0
-        return ctypes.c_void_p(t.data_ptr()), t.stride(0) if n_nodes > 1 else vocab
-
-    tp, ts = rows_of(target_probs)
-    dp, ds = rows_of(draft_probs)
-    _check(_call(dev, stream, lib().s4kv_verify_tree, _ptr(tokens, i32, "tokens"), _ptr(parents, i32, "parents"),
-                 _ptr(cu_nodes, i32, "cu_nodes"), n_nodes, batch, max_nodes, tp, ts, dp, ds, types[target_probs.dtype],
-                 vocab, _ptr(uniforms, torch.float32, "uniforms"), _ptr(path, i32, "path"),
-                 _ptr(path_len, i32, "path_len"), _ptr(next_token, i32, "next_token"),
-                 _ptr(err_flag, i32, "err_flag")), "s4kv_verify_tree")
+    tp, ts = rows_of(target_probs, "target_probs")
+    dp, ds = (None, 0) if draft_probs is None else rows_of(draft_probs, "draft_probs")
+    nodes, seqs = (n_nodes,), (batch,)
+    _call("s4kv_verify_tree", dev, stream, lib().s4kv_verify_tree, _arg(tokens, i32, nodes, dev, "tokens"),
+          _arg(parents, i32, nodes, dev, "parents"), _arg(cu_nodes, i32, (batch + 1,), dev, "cu_nodes"), n_nodes, batch,
+          max_nodes, tp, ts, dp, ds, types.index(kind), vocab, _arg(uniforms, torch.float32, nodes, dev, "uniforms"),
+          _arg(path, i32, (batch, max_nodes), dev, "path"), _arg(path_len, i32, seqs, dev, "path_len"),
+          _arg(next_token, i32, seqs, dev, "next_token"),
+          None if err_flag is None else _arg(err_flag, i32, (1,), dev, "err_flag"))
 
 
 def s4kv_append_path(cache: S4KVCache, k, v, cu_nodes, path, path_len, seq_lens, block_tables, new_lens, stream=None):
@@ -469,20 +467,14 @@ def s4kv_append_path(cache: S4KVCache, k, v, cu_nodes, path, path_len, seq_lens,
     import torch
     n_nodes = k.shape[0]
     batch, max_pages = block_tables.shape
-    kv = (n_nodes, cache.num_kv_heads, HEAD_DIM)
-    _shape(k, kv, "k")
-    _shape(v, kv, "v")
-    _shape(cu_nodes, (batch + 1,), "cu_nodes")
-    _shape(path, (batch, path.shape[-1]), "path")
-    _shape(path_len, (batch,), "path_len")
-    _shape(seq_lens, (batch,), "seq_lens")
-    _shape(new_lens, (batch,), "new_lens")
-    dev = _device(cache.pool, k, v, cu_nodes, path, path_len, seq_lens, block_tables, new_lens)
-    f16, i32 = torch.float16, torch.int32
-    _check(_call(dev, stream, lib().s4kv_append_path, cache.ref, _ptr(k, f16, "k"), _ptr(v, f16, "v"), n_nodes,
-                 _ptr(cu_nodes, i32, "cu_nodes"), _ptr(path, i32, "path"), _ptr(path_len, i32, "path_len"),
-                 path.shape[1], _ptr(seq_lens, i32, "seq_lens"), _ptr(block_tables, i32, "block_tables"), batch,
-                 max_pages, _ptr(new_lens, i32, "new_lens")), "s4kv_append_path")
+    max_nodes = path.shape[1]
+    kv, seqs = (n_nodes, cache.num_kv_heads, HEAD_DIM), (batch,)
+    f16, i32, dev = torch.float16, torch.int32, cache.pool.get_device()
+    _call("s4kv_append_path", dev, stream, lib().s4kv_append_path, cache.ref, _arg(k, f16, kv, dev, "k"),
+          _arg(v, f16, kv, dev, "v"), n_nodes, _arg(cu_nodes, i32, (batch + 1,), dev, "cu_nodes"),
+          _arg(path, i32, (batch, max_nodes), dev, "path"), _arg(path_len, i32, seqs, dev, "path_len"), max_nodes,
+          _arg(seq_lens, i32, seqs, dev, "seq_lens"), _arg(block_tables, i32, (batch, max_pages), dev, "block_tables"),
+          batch, max_pages, _arg(new_lens, i32, seqs, dev, "new_lens"))
 
 
 def s4kv_get_error(cache: S4KVCache, clear: bool = True, stream=None) -> int:

@@ -437,7 +437,8 @@ int s4kv_verify_tree(const int32_t *tokens, const int32_t *parents, const int32_
                      int max_nodes_per_seq, const void *target_probs, int64_t target_stride, const void *draft_probs,
                      int64_t draft_stride, int prob_type, int vocab, const float *uniforms, int32_t *path,
                      int32_t *path_len, int32_t *next_token, uint32_t *err_flag, void *stream) {
-  if (n_nodes < 0 || batch < 0 || max_nodes_per_seq <= 0 || vocab <= 0) return S4KV_ERR_INVALID_ARG;
+  if (n_nodes < 0 || batch < 0 || batch > (1 << 28) || max_nodes_per_seq <= 0 || vocab <= 0 || vocab > (1 << 30))
+    return S4KV_ERR_INVALID_ARG;
   if (max_nodes_per_seq > S4KV_MAX_TREE_NODES) return S4KV_ERR_UNSUPPORTED;
   if (prob_type != S4KV_PROB_F32 && prob_type != S4KV_PROB_F16 && prob_type != S4KV_PROB_BF16)
     return S4KV_ERR_INVALID_ARG;

@@ -11,187 +11,297 @@
 // held in 64 bits: a border of the cumulative sum then moves by about 1e-16 of
 // the mass whatever the order of the additions, and with it the answer.
 //
-// One CTA a sequence; the row is taken in chunks of consecutive entries whose
-// sums stay in shared memory, so that the second pass reads only the chunk that
-// holds the answer.
+// A cluster of CTAs takes a sequence, each a part of the vocabulary, and meets in
+// distributed shared memory only to add up a row.  The entries that the walk tests
+// (one a node) are fetched all at once before it, so that it runs without waiting for
+// memory.  A row is summed in chunks of 512 consecutive entries, one a warp; their sums
+// stay in shared memory, and the draw reads again only the chunk that holds its answer.
+// Bound by HBM for many sequences (one target row each, and one draft row after a
+// rejection), by the chain of a row's sum and its exchange for few.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "kernels.cuh"
 
 namespace s4kv {
 
+namespace cg = cooperative_groups;
+
 namespace {
 
-constexpr int kThreadsV = 512;
-constexpr int kPerThread = 8;
-constexpr int kChunk = kThreadsV * kPerThread;
+constexpr int kThreadsV = 256, kWarpsV = kThreadsV / 32;
+constexpr int kPerLane = 16, kBlockV = 32 * kPerLane;  // entries a warp reads at once
+constexpr int kMaxChunks = 1024;                       // chunk sums a CTA keeps
+constexpr int kMaxCluster = 8;
+constexpr unsigned kAllV = 0xFFFFFFFFu;
 
-__device__ __forceinline__ double prob(const float *p) { return static_cast<double>(*p); }
-__device__ __forceinline__ double prob(const __half *p) { return static_cast<double>(__half2float(*p)); }
-__device__ __forceinline__ double prob(const __nv_bfloat16 *p) { return static_cast<double>(__bfloat162float(*p)); }
+__device__ __forceinline__ double prob(const float *p) { return static_cast<double>(__ldg(p)); }
+__device__ __forceinline__ double prob(const __half *p) { return static_cast<double>(__half2float(__ldg(p))); }
+__device__ __forceinline__ double prob(const __nv_bfloat16 *p) { return static_cast<double>(__bfloat162float(__ldg(p))); }
 // negative entries and NaN count as 0
 __device__ __forceinline__ double positive(double x) { return x > 0.0 ? x : 0.0; }
 
-// Sum over the CTA, given to every thread; `scratch`: one double a warp.
-__device__ __forceinline__ double cta_sum(double x, double *scratch) {
+__device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
-  __syncthreads();
-  double s = 0.0;
-  for (int w = 0; w < kThreadsV / 32; ++w) s += scratch[w];
-  return s;
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(kAllV, x, off);
+  return x;
 }
 
 }  // namespace
 
+// blocks: groups of kBlockV entries in a chunk (1 but for vocabularies in the millions).
 template <typename T>
-__global__ void __launch_bounds__(kThreadsV) verify_kernel(const VerifyParams p) {
-  __shared__ int tok[S4KV_MAX_TREE_NODES], par[S4KV_MAX_TREE_NODES], out_path[S4KV_MAX_TREE_NODES];
-  __shared__ double scratch[kThreadsV / 32];
-  __shared__ int answer;
-  const int b = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kThreadsV) verify_kernel(const VerifyParams p, int blocks) {
+  __shared__ int tok[S4KV_MAX_TREE_NODES], out_path[S4KV_MAX_TREE_NODES];
+  __shared__ double at_p[S4KV_MAX_TREE_NODES], at_q[S4KV_MAX_TREE_NODES], at_u[S4KV_MAX_TREE_NODES];
+  __shared__ double chunk_sum[kMaxChunks];
+  __shared__ double part[2];  // this CTA's share of a row's sum, for two rows in turn
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int b = blockIdx.x / C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c0 = __ldg(p.cu_nodes + b), c1 = __ldg(p.cu_nodes + b + 1), n = c1 - c0;
   int32_t *path = p.path + static_cast<long>(b) * p.max_nodes;
-  const bool ok = c0 >= 0 && n >= 0 && c1 <= p.n_nodes && n <= p.max_nodes;
-  if (!ok || n == 0) {
-    if (tid < p.max_nodes) path[tid] = -1;
-    if (tid == 0) {
-      p.path_len[b] = 0;
-      p.next_token[b] = -1;
-      if (!ok) flag_error(p.err, S4KV_EFLAG_TREE);
+  const bool ok = c0 >= 0 && c1 >= c0 && c1 <= p.n_nodes && n <= p.max_nodes;
+  if (!ok || n == 0) {  // the whole cluster
+    if (rank == 0) {
+      if (tid < p.max_nodes) path[tid] = -1;
+      if (tid == 0) {
+        p.path_len[b] = 0;
+        p.next_token[b] = -1;
+        if (!ok) flag_error(p.err, S4KV_EFLAG_TREE);
+      }
     }
     return;
   }
+  const T *target = static_cast<const T *>(p.target) + static_cast<long long>(c0) * p.target_stride;
+  const T *draft = p.draft ? static_cast<const T *>(p.draft) + static_cast<long long>(c0) * p.draft_stride : nullptr;
+  const int V = p.vocab;
+
+  // ---- the entries that the walk may test
   if (tid < n) {
-    tok[tid] = __ldg(p.tokens + c0 + tid);
-    par[tid] = __ldg(p.parents + c0 + tid);
-    if (tid > 0 && static_cast<unsigned>(tok[tid]) >= static_cast<unsigned>(p.vocab)) flag_error(p.err, S4KV_EFLAG_TREE);
+    const int x = __ldg(p.tokens + c0 + tid), up = __ldg(p.parents + c0 + tid);
+    const bool known = static_cast<unsigned>(x) < static_cast<unsigned>(V);
+    if (tid > 0 && !known && rank == 0) flag_error(p.err, S4KV_EFLAG_TREE);
+    tok[tid] = known ? x : -1;
+    const bool child = known && up >= 0 && up < tid;
+    at_p[tid] = child ? positive(prob(target + up * p.target_stride + x)) : 0.0;
+    at_q[tid] = child && draft ? positive(prob(draft + up * p.draft_stride + x)) : 1.0;
+    at_u[tid] = static_cast<double>(__ldg(p.uniforms + c0 + tid));
+    out_path[tid] = -1;
   }
-  if (tid < p.max_nodes) out_path[tid] = tid == 0 ? 0 : -1;
+  // parents of nodes lane, lane + 32 (every warp walks by itself, all alike)
+  const int up0 = lane < n ? __ldg(p.parents + c0 + lane) : -1, up1 = lane + 32 < n ? __ldg(p.parents + c0 + lane + 32) : -1;
   __syncthreads();
 
-  const T *target = static_cast<const T *>(p.target), *draft = static_cast<const T *>(p.draft);
-  const int V = p.vocab;
-  int cur = 0, len = 1;
+  int cur = 0, len = 1, sums = 0;
   double M = 1.0, A = 0.0;
-  unsigned long long gone = 0;  // rejected children of cur
-  const T *P = target + static_cast<long long>(c0) * p.target_stride;
-  const T *Q = draft ? draft + static_cast<long long>(c0) * p.draft_stride : nullptr;
-  // what is left of entry v
-  auto rest = [&](int v) {
-    if (Q) return positive(positive(prob(P + v)) - A * positive(prob(Q + v)));
-    for (unsigned long long g = gone; g; g &= g - 1)
-      if (tok[__ffsll(g) - 1] == v) return 0.0;
-    return positive(prob(P + v));
-  };
-  for (int c = 1; c < n; ++c) {  // children come after their parent, in the order they are tried
-    if (par[c] != cur || static_cast<unsigned>(tok[c]) >= static_cast<unsigned>(V)) continue;
-    const double r = rest(tok[c]), u = static_cast<double>(__ldg(p.uniforms + c0 + c));
-    const double q = Q ? positive(prob(Q + tok[c])) : 1.0;
-    if (u * M * q < r) {
-      if (tid == 0) out_path[len] = c;
-      ++len;
-      cur = c;
-      M = 1.0;
-      A = 0.0;
-      gone = 0;
-      P = target + static_cast<long long>(c0 + c) * p.target_stride;
-      if (Q) Q = draft + static_cast<long long>(c0 + c) * p.draft_stride;
-    } else if (Q) {
-      A += M;
-      bool more = false;  // the new mass is needed only by another child
-      for (int d = c + 1; d < n; ++d) more |= par[d] == cur;
-      if (more) {
-        double s = 0.0;
-        for (int v = tid; v < V; v += kThreadsV) s += rest(v);
-        M = cta_sum(s, scratch);
+  unsigned long long gone = 0;  // rejected children of cur (no draft rows)
+  const T *P = target, *Q = draft;
+
+  // this CTA's chunks of a row
+  const int chunk = kBlockV * blocks;
+  const int chunks = (V - 1) / chunk + 1;
+  const int k0 = static_cast<int>(static_cast<long long>(chunks) * rank / C);
+  const int k1 = static_cast<int>(static_cast<long long>(chunks) * (rank + 1) / C);
+  // what is left of this lane's entries v0 + 32 e of a block
+  auto rest = [&](int v0, double (&x)[kPerLane]) {
+    if (Q) {
+      double q[kPerLane];
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) {
+        const int v = v0 + 32 * e + lane;
+        x[e] = v < V ? prob(P + v) : 0.0;
+        q[e] = (v < V && A > 0.0) ? prob(Q + v) : 0.0;
       }
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) x[e] = positive(positive(x[e]) - A * positive(q[e]));
     } else {
-      M -= r;
-      gone |= 1ull << c;
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) {
+        const int v = v0 + 32 * e + lane;
+        x[e] = v < V ? prob(P + v) : 0.0;
+      }
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) x[e] = positive(x[e]);
+      for (unsigned long long m = gone; m; m &= m - 1) {
+        const int x0 = tok[__ffsll(m) - 1] - v0;
+        if (x0 >= 0 && x0 < kBlockV) {
+#pragma unroll
+          for (int e = 0; e < kPerLane; ++e)
+            if (x0 == 32 * e + lane) x[e] = 0.0;
+        }
+      }
     }
+  };
+  // Sum of the rest over the row; `before`: the share of the CTAs of lower rank.  Every thread of the cluster calls it.
+  auto mass = [&](double &before) {
+    for (int k = k0 + warp; k < k1; k += kWarpsV) {
+      double s = 0.0;
+      for (int e = 0; e < blocks; ++e) {
+        double x[kPerLane];
+        rest(k * chunk + e * kBlockV, x);
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) s += x[j];
+      }
+      s = warp_sum(s);
+      if (lane == 0) chunk_sum[k - k0] = s;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      double s = 0.0;
+      for (int k = lane; k < k1 - k0; k += 32) s += chunk_sum[k];
+      s = warp_sum(s);
+      if (lane == 0) part[sums & 1] = s;
+    }
+    cluster.sync();
+    double total = 0.0;
+    for (int r = 0; r < C; ++r) {
+      if (r == rank) before = total;
+      total += *cluster.map_shared_rank(&part[sums & 1], r);
+    }
+    ++sums;  // the slot is written again only after the next sum's meeting
+    return total;
+  };
+
+  // ---- the walk
+  while (true) {
+    unsigned long long children = __ballot_sync(kAllV, up0 == cur && lane > cur) |
+                                  static_cast<unsigned long long>(__ballot_sync(kAllV, up1 == cur && lane + 32 > cur)) << 32;
+    bool moved = false;
+    while (children && !moved) {  // in the order in which they are tried
+      const int c = __ffsll(children) - 1;
+      children &= children - 1;
+      if (tok[c] < 0) continue;
+      double r = at_p[c];
+      if (Q) r = positive(r - A * at_q[c]);
+      else
+        for (unsigned long long m = gone; m; m &= m - 1)
+          if (tok[__ffsll(m) - 1] == tok[c]) r = 0.0;
+      if (at_u[c] * M * at_q[c] < r) {
+        moved = true;
+        cur = c;
+        if (tid == 0) out_path[len] = c;
+        ++len;
+        M = 1.0;
+        A = 0.0;
+        gone = 0;
+        P = target + static_cast<long long>(c) * p.target_stride;
+        if (Q) Q = draft + static_cast<long long>(c) * p.draft_stride;
+      } else if (Q) {
+        A += M;
+        double before;
+        if (children) M = mass(before);  // needed only by another child
+      } else {
+        M -= r;
+        gone |= 1ull << c;
+      }
+    }
+    if (!moved) break;
   }
 
-  // draw from the rest; where nothing is left, from cur's own row
-  auto draw = [&]() -> int {
-    double total = 0.0;
-    for (int v = tid; v < V; v += kThreadsV) total += rest(v);
-    total = cta_sum(total, scratch);
-    if (!(total > 0.0) || isinf(total)) return -1;
-    const double t = static_cast<double>(__ldg(p.uniforms + c0)) * total;
-    if (tid == 0) answer = -1;
-    double before = 0.0;
-    for (int v0 = 0; v0 < V; v0 += kChunk) {
-      const int lo = v0 + tid * kPerThread;
-      double mine = 0.0;
-      int last = -1;
-      for (int k = 0; k < kPerThread; ++k)
-        if (lo + k < V) {
-          const double r = rest(lo + k);
-          mine += r;
-          if (r > 0.0) last = lo + k;
-        }
-      const double chunk = cta_sum(mine, scratch);
-      if (before + chunk > t) {
-        // inclusive scan over the threads
-        double incl = mine;
-        for (int off = 1; off < 32; off <<= 1) {
-          const double o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-          if ((tid & 31) >= off) incl += o;
-        }
-        __syncthreads();
-        if ((tid & 31) == 31) scratch[tid >> 5] = incl;
-        __syncthreads();
-        double base = before;
-        for (int w = 0; w < (tid >> 5); ++w) base += scratch[w];
-        const double excl = base + incl - mine;
-        if (excl <= t && base + incl > t) {
-          double run = excl;
-          int hit = last;
-          for (int k = 0; k < kPerThread; ++k)
-            if (lo + k < V) {
-              run += rest(lo + k);
-              if (run > t) {
-                hit = lo + k;
-                break;
-              }
-            }
-          atomicMax(&answer, hit);
-        }
-        __syncthreads();
-        if (answer >= 0) return answer;
-      }
-      before += chunk;
-    }
-    // t reaches the end of the sum: the last entry with any mass
-    __syncthreads();
-    for (int v = tid; v < V; v += kThreadsV)
-      if (rest(v) > 0.0) atomicMax(&answer, v);
-    __syncthreads();
-    return answer;
-  };
-  int next = draw();
-  if (next < 0 && (A > 0.0 || gone)) {
+  // ---- the draw, from the rest; where nothing is left, from cur's own row
+  double before = 0.0, total = mass(before);
+  if (!(total > 0.0) && (A > 0.0 || gone)) {
     A = 0.0;
     gone = 0;
+    total = mass(before);
+  }
+  if (!(total > 0.0) || isinf(total)) {
+    if (rank == 0 && tid == 0) {
+      p.next_token[b] = -1;
+      flag_error(p.err, S4KV_EFLAG_PROBS);
+    }
+  } else {
+    double t = positive(at_u[0] * total);
+    // the CTA whose share holds t; where t is the end of the sum, the last one with any mass
+    bool holds = before <= t && before + part[(sums - 1) & 1] > t;
+    if (t >= total) {
+      int last = 0;
+      for (int r = 0; r < C; ++r)
+        if (*cluster.map_shared_rank(&part[(sums - 1) & 1], r) > 0.0) last = r;
+      holds = rank == last;
+    }
+    if (holds && warp == 0) {
+      // the chunk, then the entry: the first whose cumulative sum passes t, or the last with any mass where
+      // rounding lets none pass
+      int pick = -1, last = -1;
+      double run = before, at = before;
+      for (int k = 0; k < k1 - k0 && pick < 0; k += 32) {
+        const double x = k + lane < k1 - k0 ? chunk_sum[k + lane] : 0.0;
+        double incl = x;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const double o = __shfl_up_sync(kAllV, incl, off);
+          if (lane >= off) incl += o;
+        }
+        const unsigned hit = __ballot_sync(kAllV, x > 0.0 && run + incl > t), some = __ballot_sync(kAllV, x > 0.0);
+        if (hit) {
+          pick = k + __ffs(hit) - 1;
+          at = __shfl_sync(kAllV, run + incl - x, __ffs(hit) - 1);
+        } else if (some) {
+          last = k + 31 - __clz(some);
+        }
+        run += __shfl_sync(kAllV, incl, 31);
+      }
+      if (pick < 0) {
+        pick = last;
+        t = INFINITY;  // its last entry with any mass
+      }
+      int answer = -1;
+      last = -1;
+      for (int e = 0; e < blocks && answer < 0; ++e) {
+        const int v0 = (k0 + pick) * chunk + e * kBlockV;
+        double x[kPerLane];
+        rest(v0, x);
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+          double incl = x[j];
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const double o = __shfl_up_sync(kAllV, incl, off);
+            if (lane >= off) incl += o;
+          }
+          const unsigned hit = __ballot_sync(kAllV, x[j] > 0.0 && at + incl > t), some = __ballot_sync(kAllV, x[j] > 0.0);
+          if (hit && answer < 0) answer = v0 + 32 * j + __ffs(hit) - 1;
+          if (some) last = v0 + 32 * j + 31 - __clz(some);
+          at += __shfl_sync(kAllV, incl, 31);
+        }
+      }
+      if (lane == 0) p.next_token[b] = answer >= 0 ? answer : last;
+    }
+  }
+  if (rank == 0) {
     __syncthreads();
-    next = draw();
+    if (tid < p.max_nodes) path[tid] = tid == 0 ? 0 : tid < n ? out_path[tid] : -1;
+    if (tid == 0) p.path_len[b] = len;
   }
-  if (tid < p.max_nodes) path[tid] = out_path[tid];
-  if (tid == 0) {
-    p.path_len[b] = len;
-    p.next_token[b] = next;
-    if (next < 0) flag_error(p.err, S4KV_EFLAG_PROBS);
-  }
+  cluster.sync();  // no CTA leaves while another reads its share
+}
+
+template <typename T>
+static cudaError_t launch_verify_for(const VerifyParams &p, cudaStream_t stream) {
+  // CTAs a sequence: as many as share its row's reading while the sequences alone do not fill the card
+  // (148 SMs of 8 CTAs), and no more than there are chunks
+  int cluster = kMaxCluster;
+  while (cluster > 1 && (p.batch >= 2 * 148 * 8 / cluster || p.vocab <= kBlockV * (cluster / 2))) cluster /= 2;
+  const int blocks = static_cast<int>((static_cast<long long>(p.vocab) / cluster + 1) / (static_cast<long long>(kBlockV) * (kMaxChunks - 2)) + 1);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * cluster);
+  cfg.blockDim = dim3(kThreadsV);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T>, p, blocks);
 }
 
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
-  if (p.prob_type == S4KV_PROB_F16) verify_kernel<__half><<<p.batch, kThreadsV, 0, stream>>>(p);
-  else if (p.prob_type == S4KV_PROB_BF16) verify_kernel<__nv_bfloat16><<<p.batch, kThreadsV, 0, stream>>>(p);
-  else verify_kernel<float><<<p.batch, kThreadsV, 0, stream>>>(p);
-  return cudaGetLastError();
+  return p.prob_type == S4KV_PROB_F16 ? launch_verify_for<__half>(p, stream)
+         : p.prob_type == S4KV_PROB_BF16 ? launch_verify_for<__nv_bfloat16>(p, stream) : launch_verify_for<float>(p, stream);
 }
 
 }  // namespace s4kv

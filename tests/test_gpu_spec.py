@@ -319,6 +319,28 @@ def test_verify_large_vocabulary_and_batch():
     same(run_verify(tok, parents, cu, p, q, u, 3), verify_reference(tok, parents, cu, as_np(p), as_np(q), u, 3))
 
 
+@pytest.mark.parametrize("batch,vocab", [(149, 3000), (700, 2600), (2500, 70)])
+def test_verify_many_sequences(batch, vocab):
+    """Batches that take fewer CTAs a sequence."""
+    import torch
+    rng = np.random.default_rng(batch)
+    tok, parents, cu, p, q, u = make_verify(rng, [1 + b % 3 for b in range(batch)], vocab, 2, True, torch.float32)
+    same(run_verify(tok, parents, cu, p, q, u, 3), verify_reference(tok, parents, cu, as_np(p), as_np(q), u, 3))
+
+
+def test_verify_vocabulary_of_millions():
+    """Rows whose chunks have more than one block; the draws fall at the ends and between."""
+    import torch
+    rng = np.random.default_rng(8)
+    V = 5_000_011
+    p = torch.rand(6, V, generator=torch.Generator().manual_seed(1))
+    p /= p.sum(-1, keepdim=True)
+    tok, parents, cu = np.array([0, 9, 0, 9, 0, 9], np.int32), np.array([-1, 0] * 3, np.int32), np.array([0, 2, 4, 6], np.int32)
+    for u0 in (0.0, 0.5, 0.9999):
+        u = np.array([u0, 0.9] * 3, np.float32) * rng.random(6, dtype=np.float32)
+        same(run_verify(tok, parents, cu, p, None, u, 2), verify_reference(tok, parents, cu, as_np(p), None, u, 2))
+
+
 @pytest.mark.parametrize("u0", [0.0, float(np.float32(1) - np.float32(2) ** -24)])
 @pytest.mark.parametrize("draft", [True, False])
 def test_verify_ends_of_the_random_numbers(u0, draft):
