@@ -22,17 +22,21 @@ __global__ void __launch_bounds__(128) append_path_kernel(const PathParams p) {
   __shared__ uint8_t kc[kPage][kHeadDim];
   __shared__ uint8_t vc[kPage][kHeadDim];
 
+  __shared__ int nodes[S4KV_MAX_TREE_NODES];
+
+  // everything that depends on nothing is fetched at once: the call's time is the chain of its loads
   const int c0 = __ldg(p.cu_nodes + b), c1 = __ldg(p.cu_nodes + b + 1);
   const int m = __ldg(p.path_len + b), L = __ldg(p.seq_lens + b);
-  const int32_t *path = p.path + static_cast<long>(b) * p.max_nodes;
+  const int node = tid < p.max_nodes ? __ldg(p.path + static_cast<long>(b) * p.max_nodes + tid) : 0;
   // every CTA of the sequence comes to the same verdict on its whole path
   bool tree_ok = c0 >= 0 && c1 >= c0 && c1 <= p.n_nodes && m >= 0 && m <= p.max_nodes;
   const bool len_ok = L >= 0 && L <= p.max_pages * kPage - (tree_ok ? m : 0);
-  int node = 0;
-  if (tree_ok && tid < m) {  // m <= max_nodes <= 64
-    node = __ldg(path + tid);
-    tree_ok = node >= 0 && node < c1 - c0;
-  }
+  if (tid < p.max_nodes) nodes[tid] = node;
+  if (tid < m) tree_ok = tree_ok && node >= 0 && node < c1 - c0;  // (m <= max_nodes where the rest is right)
+  // the page that this CTA may complete
+  const int pg = len_ok ? L / kPage + slot : 0;
+  int phys = -1;
+  if (len_ok && pg < p.max_pages) phys = __ldg(p.block_tables + static_cast<long>(b) * p.max_pages + pg);
   tree_ok = __syncthreads_and(tree_ok);
   const bool first = slot == 0 && h == 0 && tid == 0;
   if (first) p.new_lens[b] = (tree_ok && len_ok) ? L + m : L;
@@ -42,21 +46,20 @@ __global__ void __launch_bounds__(128) append_path_kernel(const PathParams p) {
   }
   if (m == 0) return;
   const int end = L + m;
-  const int pg = L / kPage + slot, pl = (end - 1) / kPage;
+  const int pl = (end - 1) / kPage;
   if (pg > pl) return;
   const bool full = (pg + 1) * kPage <= end;
   if (!full && slot != 0) return;  // the partial tail belongs to slot 0
   const long res_base = (static_cast<long>(b) * H + h) * kPage * kHeadDim;
 
   if (full) {
-    const int phys = __ldg(p.block_tables + static_cast<long>(b) * p.max_pages + pg);
     const bool phys_ok = static_cast<unsigned>(phys) < static_cast<unsigned>(p.num_pages);
     for (int ch = tid; ch < kPage * (kHeadDim / 8); ch += 128) {
       const int t = ch / (kHeadDim / 8), c8 = (ch % (kHeadDim / 8)) * 8;
       const int pos = pg * kPage + t;
       const __half *sk = p.res_k + res_base + t * kHeadDim + c8, *sv = p.res_v + res_base + t * kHeadDim + c8;
       if (pos >= L) {
-        const long row = (static_cast<long>(c0 + __ldg(path + pos - L)) * H + h) * kHeadDim + c8;
+        const long row = (static_cast<long>(c0 + nodes[pos - L]) * H + h) * kHeadDim + c8;
         sk = p.k + row;
         sv = p.v + row;
       }
@@ -74,7 +77,7 @@ __global__ void __launch_bounds__(128) append_path_kernel(const PathParams p) {
     const int tail0 = max(L, pl * kPage);
     for (int ch = tid; ch < (end - tail0) * (kHeadDim / 8); ch += 128) {
       const int pos = tail0 + ch / (kHeadDim / 8), c8 = (ch % (kHeadDim / 8)) * 8;
-      const long row = (static_cast<long>(c0 + __ldg(path + pos - L)) * H + h) * kHeadDim + c8;
+      const long row = (static_cast<long>(c0 + nodes[pos - L]) * H + h) * kHeadDim + c8;
       const long dst = res_base + (pos % kPage) * kHeadDim + c8;
       *reinterpret_cast<uint4 *>(p.res_k + dst) = *reinterpret_cast<const uint4 *>(p.k + row);
       *reinterpret_cast<uint4 *>(p.res_v + dst) = *reinterpret_cast<const uint4 *>(p.v + row);

@@ -9,7 +9,9 @@
 
 namespace s4kv {
 
+template <int kBits>
 __global__ void __launch_bounds__(128) dequant_kernel(const DequantParams p) {
+  constexpr int bits = kBits;
   const int h = blockIdx.x;
   const int c = threadIdx.x;  // channel
   const int slot = blockIdx.y;
@@ -22,37 +24,46 @@ __global__ void __launch_bounds__(128) dequant_kernel(const DequantParams p) {
     }
   }
   // regions of the block: codes, then the same 768 bytes of fp16 metadata
-  const int code_bytes = kPage * kHeadDim * p.bits / 8;
+  const int code_bytes = kPage * kHeadDim * bits / 8;
   const int kcode_off = 0, vcode_off = code_bytes;
   const int kscale_off = 2 * code_bytes, kzero_off = kscale_off + 2 * kHeadDim;
   const int vscale_off = kzero_off + 2 * kHeadDim, vzero_off = vscale_off + 2 * kPage * (kHeadDim / kVGroup);
-  const uint8_t *blk = p.pool + (static_cast<long>(page) * p.num_kv_heads + h) * block_bytes_for(p.bits);
+  const uint8_t *blk = p.pool + (static_cast<long>(page) * p.num_kv_heads + h) * block_bytes_for(bits);
   const float ks = __half2float(reinterpret_cast<const __half *>(blk + kscale_off)[c]);
   const float kz = __half2float(reinterpret_cast<const __half *>(blk + kzero_off)[key_zero_slot(c)]);
   const int g = c / kVGroup;
+  // all loads before the first store: few pages cost the latency of one load, not of 16
+  float kx[kPage], vx[kPage];
+#pragma unroll
   for (int t = 0; t < kPage; ++t) {
     int kword, knib, vword, vnib;
     key_position(t, c, kword, knib);
     value_position(t, c, vword, vnib);
-    const float kcode = static_cast<float>(code_at(blk + kcode_off, kword, knib, p.bits));
-    const float vcode = static_cast<float>(code_at(blk + vcode_off, vword, vnib, p.bits));
+    const float kcode = static_cast<float>(code_at(blk + kcode_off, kword, knib, bits));
+    const float vcode = static_cast<float>(code_at(blk + vcode_off, vword, vnib, bits));
     const float vs = __half2float(reinterpret_cast<const __half *>(blk + vscale_off)[value_scale_slot(t, g)]);
     const float vz = __half2float(reinterpret_cast<const __half *>(blk + vzero_off)[g * kPage + t]);
-    const float kx = __fadd_rn(__fmul_rn(kcode, ks), kz);
-    const float vx = __fadd_rn(__fmul_rn(vcode, vs), vz);
-    const long o = ((static_cast<long>(slot) * p.num_kv_heads + h) * kPage + t) * kHeadDim + c;
+    kx[t] = __fadd_rn(__fmul_rn(kcode, ks), kz);
+    vx[t] = __fadd_rn(__fmul_rn(vcode, vs), vz);
+  }
+  const long o = (static_cast<long>(slot) * p.num_kv_heads + h) * kPage * kHeadDim + c;
+#pragma unroll
+  for (int t = 0; t < kPage; ++t) {
     if (p.out_fp32) {
-      static_cast<float *>(p.out_k)[o] = kx;
-      static_cast<float *>(p.out_v)[o] = vx;
+      static_cast<float *>(p.out_k)[o + t * kHeadDim] = kx[t];
+      static_cast<float *>(p.out_v)[o + t * kHeadDim] = vx[t];
     } else {
-      static_cast<__half *>(p.out_k)[o] = __float2half_rn(kx);
-      static_cast<__half *>(p.out_v)[o] = __float2half_rn(vx);
+      static_cast<__half *>(p.out_k)[o + t * kHeadDim] = __float2half_rn(kx[t]);
+      static_cast<__half *>(p.out_v)[o + t * kHeadDim] = __float2half_rn(vx[t]);
     }
   }
 }
 
 void launch_dequant(const DequantParams &p, cudaStream_t stream) {
-  dequant_kernel<<<dim3(p.num_kv_heads, p.n_pages), 128, 0, stream>>>(p);
+  const dim3 grid(p.num_kv_heads, p.n_pages);
+  if (p.bits == 8) dequant_kernel<8><<<grid, 128, 0, stream>>>(p);
+  else if (p.bits == 2) dequant_kernel<2><<<grid, 128, 0, stream>>>(p);
+  else dequant_kernel<4><<<grid, 128, 0, stream>>>(p);
 }
 
 }  // namespace s4kv

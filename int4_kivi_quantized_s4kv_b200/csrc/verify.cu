@@ -30,16 +30,33 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kThreadsV = 256, kWarpsV = kThreadsV / 32;
-constexpr int kPerLane = 16, kBlockV = 32 * kPerLane;  // entries a warp reads at once
+constexpr int kPerLane = 8, kBlockV = 32 * kPerLane;  // entries a warp reads at once
 constexpr int kMaxChunks = 1024;                       // chunk sums a CTA keeps
 constexpr int kMaxCluster = 8;
 constexpr unsigned kAllV = 0xFFFFFFFFu;
 
-__device__ __forceinline__ double prob(const float *p) { return static_cast<double>(__ldg(p)); }
-__device__ __forceinline__ double prob(const __half *p) { return static_cast<double>(__half2float(__ldg(p))); }
-__device__ __forceinline__ double prob(const __nv_bfloat16 *p) { return static_cast<double>(__bfloat162float(__ldg(p))); }
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 // negative entries and NaN count as 0
 __device__ __forceinline__ double positive(double x) { return x > 0.0 ? x : 0.0; }
+template <typename T>
+__device__ __forceinline__ double prob(T x) {
+  return static_cast<double>(fmaxf(as_float(x), 0.0f));  // fmaxf passes a NaN over
+}
+
+// This lane's entries v0 + 32 e of a row (0 behind its end), all loads in flight before the first is used.
+template <typename T>
+__device__ __forceinline__ void load_block(const T *row, int v0, int V, int lane, T (&x)[kPerLane]) {
+  row += v0 + lane;
+  if (v0 + kBlockV <= V) {
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) x[e] = __ldg(row + 32 * e);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) x[e] = v0 + lane + 32 * e < V ? __ldg(row + 32 * e) : T(0.0f);
+  }
+}
 
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
@@ -51,7 +68,7 @@ __device__ __forceinline__ double warp_sum(double x) {
 
 // blocks: groups of kBlockV entries in a chunk (1 but for vocabularies in the millions).
 template <typename T>
-__global__ void __launch_bounds__(kThreadsV) verify_kernel(const VerifyParams p, int blocks) {
+__global__ void __launch_bounds__(kThreadsV, 4) verify_kernel(const VerifyParams p, int blocks) {
   __shared__ int tok[S4KV_MAX_TREE_NODES], out_path[S4KV_MAX_TREE_NODES];
   __shared__ double at_p[S4KV_MAX_TREE_NODES], at_q[S4KV_MAX_TREE_NODES], at_u[S4KV_MAX_TREE_NODES];
   __shared__ double chunk_sum[kMaxChunks];
@@ -84,8 +101,8 @@ __global__ void __launch_bounds__(kThreadsV) verify_kernel(const VerifyParams p,
     if (tid > 0 && !known && rank == 0) flag_error(p.err, S4KV_EFLAG_TREE);
     tok[tid] = known ? x : -1;
     const bool child = known && up >= 0 && up < tid;
-    at_p[tid] = child ? positive(prob(target + up * p.target_stride + x)) : 0.0;
-    at_q[tid] = child && draft ? positive(prob(draft + up * p.draft_stride + x)) : 1.0;
+    at_p[tid] = child ? prob(__ldg(target + up * p.target_stride + x)) : 0.0;
+    at_q[tid] = child && draft ? prob(__ldg(draft + up * p.draft_stride + x)) : 1.0;
     at_u[tid] = static_cast<double>(__ldg(p.uniforms + c0 + tid));
     out_path[tid] = -1;
   }
@@ -105,24 +122,16 @@ __global__ void __launch_bounds__(kThreadsV) verify_kernel(const VerifyParams p,
   const int k1 = static_cast<int>(static_cast<long long>(chunks) * (rank + 1) / C);
   // what is left of this lane's entries v0 + 32 e of a block
   auto rest = [&](int v0, double (&x)[kPerLane]) {
-    if (Q) {
-      double q[kPerLane];
+    T raw[kPerLane];
+    load_block(P, v0, V, lane, raw);
+    if (Q && A > 0.0) {
+      T q[kPerLane];
+      load_block(Q, v0, V, lane, q);
 #pragma unroll
-      for (int e = 0; e < kPerLane; ++e) {
-        const int v = v0 + 32 * e + lane;
-        x[e] = v < V ? prob(P + v) : 0.0;
-        q[e] = (v < V && A > 0.0) ? prob(Q + v) : 0.0;
-      }
-#pragma unroll
-      for (int e = 0; e < kPerLane; ++e) x[e] = positive(positive(x[e]) - A * positive(q[e]));
+      for (int e = 0; e < kPerLane; ++e) x[e] = positive(prob(raw[e]) - A * prob(q[e]));
     } else {
 #pragma unroll
-      for (int e = 0; e < kPerLane; ++e) {
-        const int v = v0 + 32 * e + lane;
-        x[e] = v < V ? prob(P + v) : 0.0;
-      }
-#pragma unroll
-      for (int e = 0; e < kPerLane; ++e) x[e] = positive(x[e]);
+      for (int e = 0; e < kPerLane; ++e) x[e] = prob(raw[e]);
       for (unsigned long long m = gone; m; m &= m - 1) {
         const int x0 = tok[__ffsll(m) - 1] - v0;
         if (x0 >= 0 && x0 < kBlockV) {
