@@ -351,7 +351,7 @@ int tree_ws_layout(int num_q_heads, int num_kv_heads, int batch, int max_nodes, 
   if (max_nodes > S4KV_MAX_TREE_NODES) return S4KV_ERR_UNSUPPORTED;
   const int blocks = (max_nodes * (num_q_heads / num_kv_heads) + kTreeRows - 1) / kTreeRows;
   const unsigned long long units = static_cast<unsigned long long>(batch) * num_kv_heads * blocks;
-  if (units > 0x7FFFFFFFull) return S4KV_ERR_INVALID_ARG;
+  if (units > 0x3FFFFFFFull) return S4KV_ERR_INVALID_ARG;
   DeviceShape d;
   const int rd = device_shape(&d);
   if (rd != S4KV_OK) return rd;

@@ -12,7 +12,7 @@
 // residual rows (16), tile t >= 1 the pages 8(t-1) .. 8t-1.  The tiles of all units
 // are laid end to end and cut into one contiguous range a CTA (one persistent CTA
 // an SM), so that one long sequence fills the card; a unit cut between CTAs leaves
-// partial results, and the CTA that finishes its last piece merges them.
+// partial results, which its CTAs merge at their end, each a share of the rows.
 //
 // Tile.  Everything stands transposed: tokens (keys) or channels (values) on the
 // MMA's M = 128, query rows on N = 64, so that few rows cost little and both
@@ -77,7 +77,8 @@ constexpr uint32_t kOffRef = kOffZero + 2 * kTreeRows * 32;  // minus the refere
 constexpr uint32_t kOffRed = kOffRef + 2 * 32 * 4;           // [2][4][32] fp32
 constexpr uint32_t kOffFlag = kOffRed + 2 * 4 * 32 * 4;      // [2] last-piece flags, tensor memory's address, abort
 constexpr uint32_t kOffSplit = kOffFlag + 16;                  // the TreeSplit
-constexpr uint32_t kOffBar = kOffSplit + 16;
+constexpr uint32_t kOffCut = kOffSplit + 16;                    // [2][2] the cut units' pieces, TreeCut
+constexpr uint32_t kOffBar = kOffCut + 4 * 32;
 constexpr uint32_t kBars = 32;
 constexpr uint32_t kOffRing = kOffBar + 8 * kBars;
 static_assert(kOffQ8 % 1024 == 0 && kOffRing % 16 == 0, "operand alignment");
@@ -135,6 +136,13 @@ struct TreeWalk {
     } while (s.n == 0 && b + 1 < p.batch);
   }
 };
+
+// A unit that is cut between CTAs: where it lies, its CTAs, and this group's rows.
+struct TreeCut {
+  long long out;  // offset of the sequence's kv head in out
+  int first, last, odd, row0, rows, ticket;
+};
+static_assert(sizeof(TreeCut) == 32, "kOffCut");
 
 // The tiles 0 .. T-1 in consecutive ranges of W CTAs: the first `extra` of them take
 // each + 1 tiles, the others `each`.
@@ -215,6 +223,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   auto v_ready = [&](int x) { return bar(16 + x); };
   auto v_free = [&](int x) { return bar(18 + x); };
   const uint32_t s_full = bar(20), s_free = bar(22);
+  auto merged = [&](int g) { return bar(21 + 2 * g); };  // a group's items to merge have come
   auto p_full = [&](int x) { return bar(24 + x); };
   auto p_free = [&](int x) { return bar(26 + x); };
   auto q_full = [&](int x) { return bar(28 + x); };
@@ -294,6 +303,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     }
     mbar_init(s_full, 1);
     mbar_init(s_free, 8);
+    mbar_init(merged(0), 1);
+    mbar_init(merged(1), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -684,8 +695,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     const float sc = 4.0f * p.scale_log2;
     const uint32_t tO = tmem + kTmO + 32u * g + lane_base;
     bool ok = true;  // the group leaves together: a failed wait is told at the next vote
+    TreeCut *cuts = reinterpret_cast<TreeCut *>(sm + kOffCut) + 2 * g;
     bool first_piece = true;
-    int kt = 0;
+    int kt = 0, num_cuts = 0, merges = 0;
     while (w.rem > 0 && !failed) {
       const int t0 = w.tile, t1 = w.tile + w.take();
       const int rows = min(kGroupRows, w.s.n * G - kTreeRows * w.rb - kGroupRows * g);  // of this group
@@ -699,42 +711,60 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       }
       uint32_t seen = 0;  // tile 0: the rows that see this token
       if (t0 == 0 && rows > 0) {
-        // ancestors of nodes lane and lane + 32, themselves among them, by pointer doubling
-        int up[2];
-        unsigned long long anc[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int a = lane + 32 * e;
-          up[e] = a < w.s.n ? __ldg(p.parents + w.s.c0 + a) : -1;
-          if (up[e] < -1 || up[e] >= a) {
-            if (a < w.s.n) flag_error(p.err, S4KV_EFLAG_TREE);
-            up[e] = -1;
-          }
-          anc[e] = 1ull << a;
-        }
-#pragma unroll 1
-        for (int s = 0; s < 6; ++s) {
-          unsigned long long m[2];
-          int u[2];
+        if (wq < 2) {
+          // ancestors of nodes lane and lane + 32, themselves among them, by pointer doubling
+          int up[2];
+          unsigned long long anc[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const unsigned long long m0 = __shfl_sync(kAll, anc[0], up[e] & 31), m1 = __shfl_sync(kAll, anc[1], up[e] & 31);
-            const int u0 = __shfl_sync(kAll, up[0], up[e] & 31), u1 = __shfl_sync(kAll, up[1], up[e] & 31);
-            m[e] = up[e] < 0 ? 0ull : up[e] < 32 ? m0 : m1;
-            u[e] = up[e] < 0 ? -1 : up[e] < 32 ? u0 : u1;
+            const int a = lane + 32 * e;
+            up[e] = a < w.s.n ? __ldg(p.parents + w.s.c0 + a) : -1;
+            if (up[e] < -1 || up[e] >= a) {
+              if (a < w.s.n) flag_error(p.err, S4KV_EFLAG_TREE);
+              up[e] = -1;
+            }
+            anc[e] = 1ull << a;
           }
-          anc[0] |= m[0];
-          anc[1] |= m[1];
-          up[0] = u[0];
-          up[1] = u[1];
-        }
 #pragma unroll 1
-        for (int j = 0; j < 32; ++j) {
-          const int node = j < rows ? (kTreeRows * w.rb + kGroupRows * g + j) / G : 0;
-          const unsigned long long m0 = __shfl_sync(kAll, anc[0], node & 31), m1 = __shfl_sync(kAll, anc[1], node & 31);
-          const unsigned long long m = node < 32 ? m0 : m1;
-          const bool s = tl < 64 ? (m >> tl) & 1 : tl - 64 < w.s.L % kPage;
-          seen |= (s ? 1u : 0u) << j;
+          for (int s = 1; s < w.s.n; s <<= 1) {
+            unsigned long long m[2];
+            int u[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const unsigned long long m0 = __shfl_sync(kAll, anc[0], up[e] & 31), m1 = __shfl_sync(kAll, anc[1], up[e] & 31);
+              const int u0 = __shfl_sync(kAll, up[0], up[e] & 31), u1 = __shfl_sync(kAll, up[1], up[e] & 31);
+              m[e] = up[e] < 0 ? 0ull : up[e] < 32 ? m0 : m1;
+              u[e] = up[e] < 0 ? -1 : up[e] < 32 ? u0 : u1;
+            }
+            anc[0] |= m[0];
+            anc[1] |= m[1];
+            up[0] = u[0];
+            up[1] = u[1];
+          }
+          // transposed: the nodes that have token 32 wq + lane among them
+          const uint32_t a0 = static_cast<uint32_t>(anc[0] >> (32 * wq)), a1 = static_cast<uint32_t>(anc[1] >> (32 * wq));
+          uint32_t d0 = 0, d1 = 0;
+#pragma unroll 4
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t b0 = __ballot_sync(kAll, a0 >> j & 1), b1 = __ballot_sync(kAll, a1 >> j & 1);
+            if (lane == j) {
+              d0 = b0;
+              d1 = b1;
+            }
+          }
+          // and from nodes to rows; rows that the unit does not have see token 0, so that their sums are finite
+          int node = (kTreeRows * w.rb + kGroupRows * g) / G, head = kTreeRows * w.rb + kGroupRows * g - node * G;
+#pragma unroll 4
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t s = j < rows ? (node < 32 ? d0 >> node : d1 >> (node - 32)) : (tl == 0 ? 1u : 0u);
+            seen |= (s & 1u) << j;
+            if (++head == G) {
+              head = 0;
+              ++node;
+            }
+          }
+        } else {
+          seen = tl - 64 < w.s.L % kPage ? 0xFFFFFFFFu : 0u;  // the residual rows
         }
       }
       for (int t = t0; t < t1; ++t, ++kt) {
@@ -742,10 +772,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         ok = ok && wait_warp(s_full, kt & 1);
         if (rows <= 0) {  // nothing to do but to keep the barriers' counts
           ok = ok && (kt < 2 || wait_warp(p_free(x2), prev2(kt)));
-          if (!ok) {
-            fail();
-            break;
-          }
+          if (!ok) *abort_flag = 1;  // the group leaves at its next vote
           if (lane == 0) {
             mbar_arrive(s_free);
             mbar_arrive(p_full(x2));
@@ -898,46 +925,132 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           if (wq == 0) p.part_ml[slot * kTreeRows + kGroupRows * g + lane] = make_float2(myref, lsum);
           __threadfence();
           group_sync(bid);
-          const TreeSplit split = *reinterpret_cast<const TreeSplit *>(sm + kOffSplit);
-          const int wf = split.cta_of(w.start), wl = split.cta_of(w.start + w.s.tiles - 1);
-          const int rbs = (p.max_nodes * G + kTreeRows - 1) / kTreeRows;
-          uint32_t *ticket = p.tickets + ((static_cast<long>(w.b) * H + w.h) * rbs + w.rb) * 2 + g;
           if (wq == 0 && lane == 0) {
-            const bool last = atomicAdd(ticket, 1u) + 1 == static_cast<uint32_t>(wl - wf + 1);
-            if (last) *ticket = 0u;
-            *last_flag = last;
+            const TreeSplit split = *reinterpret_cast<const TreeSplit *>(sm + kOffSplit);
+            TreeCut c;
+            c.out = (static_cast<long long>(w.s.c0) * p.num_q_heads + w.h * G) * kHeadDim;
+            c.first = split.cta_of(w.start);
+            c.last = split.cta_of(w.start + w.s.tiles - 1);
+            c.odd = split.first(c.first) < w.start;
+            c.row0 = row0;
+            c.rows = rows;
+            c.ticket = ((w.b * H + w.h) * ((p.max_nodes * G + kTreeRows - 1) / kTreeRows) + w.rb) * 2 + g;
+            cuts[num_cuts] = c;
+            atomicAdd(p.tickets + c.ticket, 1u);
           }
-          group_sync(bid);
-          if (*last_flag) {
-            // merge the unit's pieces in their order: lane j the sums of row j, every thread its channel of all rows
-            __threadfence();
-            const int odd = split.first(wf) < w.start;  // the unit is the last of its first CTA's pieces
-            auto slot_of = [&](int c) { return (2ll * c + (c == wf ? odd : 0)) * kTreeRows + kGroupRows * g; };
-            float M = -INFINITY, sum = 0.f;
-#pragma unroll 4
-            for (int c = wf; c <= wl; ++c) M = fmaxf(M, __ldcg(p.part_ml + slot_of(c) + lane).x);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0.f;
-#pragma unroll 1
-            for (int c = wf; c <= wl; ++c) {
-              const long long at = slot_of(c);
-              const float *src = p.part + at * kHeadDim + ch;
-              float v[32];  // rows that the unit does not have hold anything and are not stored
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __ldcg(src + j * kHeadDim);
-              const float2 ml = __ldcg(p.part_ml + at + lane);
-              const float wt = fast_exp2(ml.x - M);
-              sum += wt * ml.y;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] += __shfl_sync(kAll, wt, j) * v[j];
-            }
-            store(1.0f / sum);
-          }
-          group_sync(bid);  // the flag is read before another piece sets it
+          ++num_cuts;
         }
       }
       first_piece = false;
       w.next(p);
+    }
+
+    // ---- units that are cut between CTAs: each of a unit's CTAs merges its share of the rows once all pieces are
+    // there (all CTAs are resident, and each has told of its pieces before it waits here)
+    // (a group without rows in the last unit has not waited for that unit's last product, which reads both groups' weights)
+    ok = ok && wait_warp(p_free((kt - 1) & 1), ((kt - 1) >> 1) & 1);
+    if (!failed && group_any(bid, !ok)) fail();
+    for (int x = 0; x < num_cuts && !failed; ++x) {
+      const TreeCut c = cuts[x];
+      const int pieces = c.last - c.first + 1, mine = static_cast<int>(blockIdx.x) - c.first;
+      uint32_t *ticket = p.tickets + c.ticket;
+      if (wq == 0 && lane == 0) {
+        const long long begun = clock64();
+        uint32_t there;
+        while (true) {
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(ticket) : "memory");
+          if (static_cast<int>(there & 0xFFFFu) >= pieces || clock64() - begun > kAbortWaitCycles) break;
+          __nanosleep(100);  // the counter's line is everybody's
+        }
+        *last_flag = static_cast<int>(there & 0xFFFFu) >= pieces;
+      }
+      group_sync(bid);
+      if (!*last_flag) {
+        fail();
+        break;
+      }
+      __threadfence();
+      const int ch = 32 * wq + 4 * (lane & 7) + 2 * (lane >> 4) + (lane >> 3 & 1);
+      auto slot_of = [&](int k) { return (2ll * (c.first + k) + (k == 0 ? c.odd : 0)) * kTreeRows + kGroupRows * g; };
+      // its items, (row, piece) pairs with the pieces of a row in their order, come by bulk copies, 64 at a time into the
+      // 32 KB where the weights were: one wait for other SMs' writes, whether they are few rows of many pieces or many of few
+      const int lo = c.rows * mine / pieces, items = (c.rows * (mine + 1) / pieces - lo) * pieces;
+      const uint32_t s_items = base + kOffP + 2 * g * kPBytes;
+      float *ml = reinterpret_cast<float *>(sm + kOffQ8 + g * kQ8Bytes);  // [items], items < 32 + pieces
+      const float *vals = reinterpret_cast<const float *>(sm + kOffP + 2 * g * kPBytes);
+      auto fetch = [&](int y0) {
+        const int count = min(64, items - y0);
+        if (wq == 0 && count > 0) {
+          asm volatile("fence.proxy.async;" ::: "memory");  // plain stores (other SMs' to the pieces, this one's to the weights) before the copies
+          if (lane == 0) mbar_arrive_expect_tx(merged(g), count * kHeadDim * 4);
+          __syncwarp();
+          for (int y = lane; y < count; y += 32)
+            bulk_copy_g2s(s_items + y * kHeadDim * 4, p.part + (slot_of((y0 + y) % pieces) + lo + (y0 + y) / pieces) * kHeadDim,
+                          kHeadDim * 4, merged(g));
+        }
+      };
+      fetch(0);
+      // ml[row][piece] = the piece's weight: many rows of few pieces a thread each, few rows of many pieces a warp each
+      if (pieces <= 4) {
+        if (tl * pieces < items) {
+          float2 x[4];
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[k] = k < pieces ? __ldcg(p.part_ml + slot_of(k) + lo + tl) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = fmaxf(top, x[k].x);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum += (x[k].x = fast_exp2(x[k].x - top)) * x[k].y;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < pieces) ml[tl * pieces + k] = x[k].x / sum;
+        }
+      } else for (int r = wq; r * pieces < items; r += 4) {
+        float M = -INFINITY, sum = 0.f;
+        for (int y = lane; y < pieces; y += 32) {
+          const float2 x = __ldcg(p.part_ml + slot_of(y) + lo + r);
+          const float top = fmaxf(M, x.x);
+          sum = sum * fast_exp2(M - top) + x.y * fast_exp2(x.x - top);
+          M = top;
+          ml[r * pieces + y] = x.x;
+        }
+        float top = M;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+        sum = lane < pieces ? sum * fast_exp2(M - top) : 0.f;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+        for (int y = lane; y < pieces; y += 32) ml[r * pieces + y] = fast_exp2(ml[r * pieces + y] - top) / sum;
+      }
+      group_sync(bid);
+      int k = 0, row = c.row0 + lo;
+      float acc = 0.f;
+      for (int y0 = 0; y0 < items; y0 += 64) {
+        ok = ok && wait_warp(merged(g), merges & 1);
+        ++merges;
+        const int count = ok ? min(64, items - y0) : 0;
+#pragma unroll 4
+        for (int y = 0; y < count; ++y) {
+          acc += ml[y0 + y] * vals[y * kHeadDim + ch];
+          if (++k == pieces) {
+            const int node = row / G;
+            p.out[c.out + (static_cast<long long>(node) * p.num_q_heads + (row - node * G)) * kHeadDim + ch] = __float2half_rn(acc);
+            acc = 0.f;
+            k = 0;
+            ++row;
+          }
+        }
+        group_sync(bid);  // the items have been read
+        fetch(y0 + 64);
+      }
+      if (group_any(bid, !ok)) {
+        fail();
+        break;
+      }
+      group_sync(bid);
+      // the last of them leaves the counter at zero
+      if (wq == 0 && lane == 0 && (atomicAdd(ticket, 0x10000u) >> 16) + 1 == static_cast<uint32_t>(pieces)) *ticket = 0u;
     }
   }
 
@@ -955,8 +1068,18 @@ static cudaError_t launch_tree_for(const TreeParams &p, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(tree_kernel<kBits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(Ring<kBits>::kSmem));
   if (e != cudaSuccess) return e;
-  tree_kernel<kBits><<<p.num_ctas, kTreeThreads, Ring<kBits>::kSmem, stream>>>(p);
-  return cudaGetLastError();
+  // a cooperative launch: CTAs that share a unit wait for one another at its end
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_ctas));
+  cfg.blockDim = dim3(kTreeThreads);
+  cfg.dynamicSmemBytes = Ring<kBits>::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_kernel<kBits>, p);
 }
 
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream) {
