@@ -39,6 +39,8 @@
 //
 // Bound by HBM when R = nodes x G is small (176 bytes of int4 cache a token feed 512 R
 // operations), by the MMAs and the shared-memory port for many rows.
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "tc05.cuh"
 
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             }
           } else {
             // two pages a warp, half of a page's tiles at a time
-#pragma unroll 1
+#pragma unroll 2
             for (int ph = 0; ph < 4; ++ph) {
               const int pg = 2 * wq + (ph >> 1), hf = ph & 1;
               if (pg >= np) break;  // the lanes of missing pages hold what they held: their logits are masked
@@ -788,7 +790,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         // logits in log2 units minus the reference; -inf where this token is not seen
         const uint32_t mask = t == 0 ? seen : (tl / kPage < w.pages(t) ? 0xFFFFFFFFu : 0u);
         const bool masked = __any_sync(kAll, mask != 0xFFFFFFFFu);
-        auto shift = [&]() {
+        auto shift_as = [&](auto with_mask) {
           float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
@@ -796,7 +798,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             float2 a = make_float2(sv[j], sv[j + 1]), b = make_float2(sv[j + 2], sv[j + 3]);
             a = fma2(a, make_float2(sc, sc), make_float2(__uint_as_float(r.x), __uint_as_float(r.y)));
             b = fma2(b, make_float2(sc, sc), make_float2(__uint_as_float(r.z), __uint_as_float(r.w)));
-            if (masked) {
+            if (with_mask.value) {
               a.x = mask >> j & 1 ? a.x : -INFINITY;
               a.y = mask >> (j + 1) & 1 ? a.y : -INFINITY;
               b.x = mask >> (j + 2) & 1 ? b.x : -INFINITY;
@@ -811,6 +813,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           }
           return fmaxf(m0, m1);
         };
+        auto shift = [&]() { return masked ? shift_as(std::true_type()) : shift_as(std::false_type()); };
         load();
         const float top = shift();
         if (group_any(bid, top > kRefSlack || t == t0 || !ok)) {
