@@ -39,6 +39,7 @@
 //
 // Bound by HBM when R = nodes x G is small (176 bytes of int4 cache a token feed 512 R
 // operations), by the MMAs and the shared-memory port for many rows.
+#include <cfloat>
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -80,7 +81,8 @@ constexpr uint32_t kOffRed = kOffRef + 2 * 32 * 4;           // [2][4][32] fp32
 constexpr uint32_t kOffFlag = kOffRed + 2 * 4 * 32 * 4;      // [2] last-piece flags, tensor memory's address, abort
 constexpr uint32_t kOffSplit = kOffFlag + 16;                  // the TreeSplit
 constexpr uint32_t kOffCut = kOffSplit + 16;                    // [2][2] the cut units' pieces, TreeCut
-constexpr uint32_t kOffBar = kOffCut + 4 * 32;
+constexpr uint32_t kOffOdd = kOffCut + 4 * 32;                 // [4 pieces][4 V warps] drafted values that are not finite
+constexpr uint32_t kOffBar = kOffOdd + 64;
 constexpr uint32_t kBars = 32;
 constexpr uint32_t kOffRing = kOffBar + 8 * kBars;
 static_assert(kOffQ8 % 1024 == 0 && kOffRing % 16 == 0, "operand alignment");
@@ -565,6 +567,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             return res + res_base;
           };
           if (is_v) {
+            // a drafted value that is not finite must not reach the rows that do not see it, and 0 * infinity would: it
+            // is taken as 0 here and added at the end to the rows that do
+            bool odd = false;
+            auto finite = [&](uint32_t x) {
+              const uint32_t e = x & 0x7C007C00u;
+              if ((e & 0xFFFFu) == 0x7C00u) x &= 0xFFFF0000u, odd = true;
+              if ((e >> 16) == 0x7C00u) x &= 0x0000FFFFu, odd = true;
+              return x;
+            };
 #pragma unroll 1
             for (int pb = 0; pb < kTilePages; pb += 4) {
               uint32_t o0[16], o1[16];
@@ -578,6 +589,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
                 for (int e = 0; e < 4; ++e) {
                   const int tk = 2 * i + (e & 1) + 8 * (e >> 1);
                   x[e] = tk < count ? *reinterpret_cast<const uint2 *>(rv + tk * stride + 32 * wq + 4 * n) : make_uint2(0, 0);
+                  if (pb == 0) x[e] = make_uint2(finite(x[e].x), finite(x[e].y));
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -590,6 +602,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
               tc05::tmem_st_frag16(tV + lane_base + 8 * pb, o0);
               tc05::tmem_st_frag16(tV + lane_base + (16u << 16) + 8 * pb, o1);
             }
+            odd = __any_sync(kAll, odd);
+            if (lane == 0) reinterpret_cast<volatile int *>(sm + kOffOdd)[4 * (uc & 3) + wq] = odd;
           } else {
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
@@ -699,7 +713,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     bool ok = true;  // the group leaves together: a failed wait is told at the next vote
     TreeCut *cuts = reinterpret_cast<TreeCut *>(sm + kOffCut) + 2 * g;
     bool first_piece = true;
-    int kt = 0, num_cuts = 0, merges = 0;
+    int kt = 0, uc = 0, num_cuts = 0, merges = 0;
     while (w.rem > 0 && !failed) {
       const int t0 = w.tile, t1 = w.tile + w.take();
       const int rows = min(kGroupRows, w.s.n * G - kTreeRows * w.rb - kGroupRows * g);  // of this group
@@ -902,6 +916,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         }
         const int row0 = kTreeRows * w.rb + kGroupRows * g;
         const int ch = 32 * wq + 4 * (lane & 7) + 2 * (lane >> 4) + (lane >> 3 & 1);  // the channel of this lane
+        if (t0 == 0 && reinterpret_cast<volatile int *>(sm + kOffOdd)[4 * (uc & 3) + wq]) {
+          // drafted values that are not finite, to the rows that see them: +infinity in `more`, -infinity in `less`, NaN in both
+          uint32_t more = 0, less = 0;
+#pragma unroll 1
+          for (int j = 0; j < rows; ++j)
+            for (int a = (row0 + j) / G; a >= 0;) {
+              const float x = __half2float(p.v[(static_cast<long>(w.s.c0 + a) * H + w.h) * kHeadDim + ch]);
+              if (!(x <= FLT_MAX)) more |= 1u << j;
+              if (!(x >= -FLT_MAX)) less |= 1u << j;
+              const int up = __ldg(p.parents + w.s.c0 + a);
+              a = up < a ? up : -1;
+            }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (more >> j & 1) o[j] += INFINITY;
+            if (less >> j & 1) o[j] -= INFINITY;
+          }
+        }
         // out of row j = o[j] times lane j's factor
         auto store = [&](float factor) {
           int head = row0 % G;
@@ -945,6 +977,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         }
       }
       first_piece = false;
+      ++uc;
       w.next(p);
     }
 

@@ -124,6 +124,41 @@ def test_tree_attention_logits_far_apart():
     close(run_tree(c, q, k, v, cu, parents), ref, bound)
 
 
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("length", [0, 5, 300])
+def test_tree_attention_values_that_are_not_finite(bad, length):
+    """A drafted token with an infinity or NaN in its key or value reaches the rows that see it, and no others."""
+    rng = np.random.default_rng(21)
+    nodes = [40, 9]
+    c = SpecCache([length, 70], 2, 4, seed=22)
+    cu, parents, q, k, v = make_tree(rng, nodes, 2, 4, c.key_scale, 3)
+    ref, bound = tree_reference(c, q, k, v, cu, parents)
+    who = {}  # node -> the rows that see it, as node numbers
+    for b in range(2):
+        for i in range(nodes[b]):
+            a = i
+            while a >= 0:
+                who.setdefault(cu[b] + a, []).append(cu[b] + i)
+                a = parents[cu[b] + a]
+    x = int(cu[0]) + 33
+    seen = np.zeros(len(q), bool)
+    seen[who[x]] = True
+    assert 0 < seen.sum() < 40
+    wrong = v.copy()
+    wrong[x, 1, 77] = bad
+    out = run_tree(c, q, k, wrong, cu, parents).float().cpu().numpy().astype(np.float64)
+    hit = np.zeros(out.shape, bool)
+    hit[seen, 4:, 77] = True  # query heads 4 - 7 read kv head 1
+    assert np.array_equal(out[hit], np.full(hit.sum(), bad), equal_nan=True)
+    assert (np.abs(out - ref)[~hit] <= bound[~hit]).all()
+    wrong = k.copy()
+    wrong[x, 0, 5] = bad
+    out = run_tree(c, q, wrong, v, cu, parents).float().cpu().numpy().astype(np.float64)
+    hit = np.zeros(out.shape, bool)
+    hit[seen, :4] = True
+    assert (np.abs(out - ref)[~hit] <= bound[~hit]).all()
+
+
 def test_tree_attention_leaves_other_rows():
     import torch
     rng = np.random.default_rng(8)
