@@ -11,8 +11,9 @@
 // head); its keys come in tiles of 128: tile 0 holds the drafted tokens (64) and the
 // residual rows (16), tile t >= 1 the pages 8(t-1) .. 8t-1.  The tiles of all units
 // are laid end to end and cut into one contiguous range a CTA (one persistent CTA
-// an SM), so that one long sequence fills the card; a unit cut between CTAs leaves
-// partial results, which its CTAs merge at their end, each a share of the rows.
+// an SM) -- or, where there are fewer units than CTAs, each unit into parts -- so that one
+// long sequence fills the card; a unit cut between CTAs leaves partial results, which
+// its CTAs merge at their end, each a share of the rows.
 //
 // Tile.  Everything stands transposed: tokens (keys) or channels (values) on the
 // MMA's M = 128, query rows on N = 64, so that few rows cost little and both
@@ -56,8 +57,11 @@ constexpr int kTreeThreads = 32 * 20;  // 5 warps a scheduler: 96 registers a th
 constexpr int kTile = 128;                 // keys a tile
 constexpr int kTilePages = kTile / kPage;  // 8
 constexpr int kGroupRows = 32;             // query rows of a softmax group
+// CTAs a unit at most, and tiles a CTA at least where there are more CTAs than units: a tile takes about 1.5 us, a merge
+// as long as 3 to 5 tiles, and longer for many pieces.
+constexpr int kMaxPieces = 40;
 #ifndef S4KV_TREE_MIN_TILES
-#define S4KV_TREE_MIN_TILES 2  // the fewest tiles a CTA is given
+#define S4KV_TREE_MIN_TILES 3
 #endif
 constexpr float kRefSlack = 14.0f;         // log2 slack of the softmax reference: weights up to 2^14, finite in fp16
 constexpr float kZeroUnit = 0x1p-10f;      // zero-point shares enter as share * 2^-10 (fp16) against 2^8, in units of 4
@@ -80,7 +84,7 @@ constexpr uint32_t kOffRef = kOffZero + 2 * kTreeRows * 32;  // minus the refere
 constexpr uint32_t kOffRed = kOffRef + 2 * 32 * 4;           // [2][4][32] fp32
 constexpr uint32_t kOffFlag = kOffRed + 2 * 4 * 32 * 4;      // [2] last-piece flags, tensor memory's address, abort
 constexpr uint32_t kOffSplit = kOffFlag + 16;                  // the TreeSplit
-constexpr uint32_t kOffCut = kOffSplit + 16;                    // [2][2] the cut units' pieces, TreeCut
+constexpr uint32_t kOffCut = kOffSplit + 32;                    // [2][2] the cut units' pieces, TreeCut
 constexpr uint32_t kOffOdd = kOffCut + 4 * 32;                 // [4 pieces][4 V warps] drafted values that are not finite
 constexpr uint32_t kOffBar = kOffOdd + 64;
 constexpr uint32_t kBars = 32;
@@ -148,12 +152,14 @@ struct TreeCut {
 };
 static_assert(sizeof(TreeCut) == 32, "kOffCut");
 
-// The tiles 0 .. T-1 in consecutive ranges of W CTAs: the first `extra` of them take
-// each + 1 tiles, the others `each`.
+// How the units' tiles are dealt out.  With at least as many CTAs as units, a CTA takes a part of one unit (first ..
+// last: its unit's CTAs), so that none has two beginnings and ends; the CTAs that units leave over are shared out by
+// tiles.  With fewer, the tiles 0 .. T-1 of all units go to W CTAs in consecutive ranges, the first `extra` of `each` + 1
+// tiles, the others of `each`.
 struct TreeSplit {
-  long long each;
-  int extra;
-  __device__ __forceinline__ long long first(int c) const { return c * each + min(c, extra); }
+  long long each;  // 0: parts of one unit
+  int extra, first, last;
+  __device__ __forceinline__ long long begin(int c) const { return c * each + min(c, extra); }
   __device__ __forceinline__ int cta_of(long long x) const {
     const long long longer = extra * (each + 1);
     return static_cast<int>(x < longer ? div(x, each + 1) : extra + div(x - longer, each));
@@ -161,6 +167,12 @@ struct TreeSplit {
   // 64-bit quotients are slow and next to never needed
   static __device__ __forceinline__ long long div(long long x, long long y) {
     return ((x | y) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+  }
+  // CTAs of a unit of `tiles` tiles where T tiles in `units` units meet `ctas` >= units CTAs: all units' together are
+  // at most ctas
+  static __device__ __forceinline__ int parts(int tiles, long long T, long long units, int ctas) {
+    const int c = 1 + static_cast<int>(div((ctas - units) * tiles, T));
+    return max(1, min(c, min(kMaxPieces, tiles / S4KV_TREE_MIN_TILES)));
   }
 };
 
@@ -238,28 +250,50 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   {
     const int per = (B + 31) >> 5;
     const int b_lo = min(B, lane * per), b_hi = min(B, b_lo + per);
-    long long sum = 0;
+    long long sum = 0, units = 0;
     uint32_t bad = 0;
+    // (a batch of up to 32 has one sequence a lane, read once)
+    const TreeSeq mine0 = tree_seq(p, min(b_lo, B - 1));
+    auto seq = [&](int b) { return b == b_lo ? mine0 : tree_seq(p, b); };
     for (int b = b_lo; b < b_hi; ++b) {
-      const TreeSeq s = tree_seq(p, b);
+      const TreeSeq s = seq(b);
       bad |= s.bad;
       sum += static_cast<long long>(s.tiles) * s.blocks * H;
+      units += static_cast<long long>(s.blocks) * H;
     }
     if (blockIdx.x == 0 && warp == 0 && bad) flag_error(p.err, bad);
+    long long T = sum;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      T += __shfl_xor_sync(kAll, T, off);
+      units += __shfl_xor_sync(kAll, units, off);
+    }
+    if (T == 0) return;
+    const bool parts = units <= p.num_ctas;
+    // what is scanned: a sequence's CTAs or its tiles
+    auto share_of = [&](const TreeSeq &s) {
+      return static_cast<long long>(s.blocks) * H * (parts && s.tiles > 0 ? TreeSplit::parts(s.tiles, T, units, p.num_ctas) : s.tiles);
+    };
+    if (parts) {
+      sum = 0;
+      for (int b = b_lo; b < b_hi; ++b) sum += share_of(seq(b));
+    }
     long long incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const long long t = __shfl_up_sync(kAll, incl, off);
       if (lane >= off) incl += t;
     }
-    const long long T = __shfl_sync(kAll, incl, 31);
-    const int W = static_cast<int>(min(static_cast<long long>(p.num_ctas), (T + S4KV_TREE_MIN_TILES - 1) / S4KV_TREE_MIN_TILES));
+    const int W = parts ? static_cast<int>(__shfl_sync(kAll, incl, 31)) : p.num_ctas;
     if (static_cast<int>(blockIdx.x) >= W) return;  // the whole CTA
-    TreeSplit split;
-    split.each = TreeSplit::div(T, W);
-    split.extra = static_cast<int>(T - split.each * W);
-    const long long s0 = split.first(blockIdx.x), s1 = split.first(blockIdx.x + 1);
-    if (tid == 0) *reinterpret_cast<TreeSplit *>(sm + kOffSplit) = split;  // for the merge of cut units
+    TreeSplit split = {0, 0, 0, 0};
+    long long s0 = blockIdx.x;
+    if (!parts) {
+      split.each = TreeSplit::div(T, W);
+      split.extra = static_cast<int>(T - split.each * W);
+      s0 = split.begin(blockIdx.x);
+      w.rem = static_cast<int>(split.begin(blockIdx.x + 1) - s0);
+    }
     const long long excl = incl - sum;
     const unsigned hit = __ballot_sync(kAll, excl <= s0 && s0 < incl);
     const int src = __ffs(hit) - 1;
@@ -267,8 +301,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     long long pre = excl;
     if (lane == src) {
       for (bs = b_lo; bs < b_hi; ++bs) {
-        const TreeSeq s = tree_seq(p, bs);
-        const long long mine = static_cast<long long>(s.tiles) * s.blocks * H;
+        const long long mine = share_of(seq(bs));
         if (s0 < pre + mine) break;
         pre += mine;
       }
@@ -276,12 +309,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     w.b = __shfl_sync(kAll, bs, src);
     pre = __shfl_sync(kAll, pre, src);
     w.s = tree_seq(p, w.b);
-    const int u = static_cast<int>(TreeSplit::div(s0 - pre, w.s.tiles));
+    const int each = parts ? TreeSplit::parts(w.s.tiles, T, units, p.num_ctas) : w.s.tiles;
+    const int u = static_cast<int>(TreeSplit::div(s0 - pre, each)), k = static_cast<int>(s0 - pre - static_cast<long long>(u) * each);
     w.h = u / w.s.blocks;
     w.rb = u - w.h * w.s.blocks;
-    w.start = pre + static_cast<long long>(u) * w.s.tiles;
-    w.tile = static_cast<int>(s0 - w.start);
-    w.rem = static_cast<int>(s1 - s0);
+    w.start = pre + static_cast<long long>(u) * each;
+    w.tile = k;
+    if (parts) {  // part k of the unit
+      split.first = static_cast<int>(blockIdx.x) - k;
+      split.last = split.first + each - 1;
+      w.tile = static_cast<int>(TreeSplit::div(static_cast<long long>(w.s.tiles) * k, each));
+      w.rem = static_cast<int>(TreeSplit::div(static_cast<long long>(w.s.tiles) * (k + 1), each)) - w.tile;
+    }
+    if (tid == 0) *reinterpret_cast<TreeSplit *>(sm + kOffSplit) = split;  // for the merge of cut units
   }
 
   // ---- setup
@@ -964,9 +1004,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             const TreeSplit split = *reinterpret_cast<const TreeSplit *>(sm + kOffSplit);
             TreeCut c;
             c.out = (static_cast<long long>(w.s.c0) * p.num_q_heads + w.h * G) * kHeadDim;
-            c.first = split.cta_of(w.start);
-            c.last = split.cta_of(w.start + w.s.tiles - 1);
-            c.odd = split.first(c.first) < w.start;
+            c.first = split.each ? split.cta_of(w.start) : split.first;
+            c.last = split.each ? split.cta_of(w.start + w.s.tiles - 1) : split.last;
+            c.odd = split.each && split.begin(c.first) < w.start;
             c.row0 = row0;
             c.rows = rows;
             c.ticket = ((w.b * H + w.h) * ((p.max_nodes * G + kTreeRows - 1) / kTreeRows) + w.rb) * 2 + g;
@@ -1012,7 +1052,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       // 32 KB where the weights were: one wait for other SMs' writes, whether they are few rows of many pieces or many of few
       const int lo = c.rows * mine / pieces, items = (c.rows * (mine + 1) / pieces - lo) * pieces;
       const uint32_t s_items = base + kOffP + 2 * g * kPBytes;
-      float *ml = reinterpret_cast<float *>(sm + kOffQ8 + g * kQ8Bytes);  // [items], items < 32 + pieces
+      float *ml = reinterpret_cast<float *>(sm + kOffQ8 + g * kQ8Bytes);  // [items], fewer than 32 + pieces of them
       const float *vals = reinterpret_cast<const float *>(sm + kOffP + 2 * g * kPBytes);
       auto fetch = [&](int y0) {
         const int count = min(64, items - y0);
