@@ -11,7 +11,7 @@
 // head); its keys come in tiles of 128: tile 0 holds the drafted tokens (64) and the
 // residual rows (16), tile t >= 1 the pages 8(t-1) .. 8t-1.  The tiles of all units
 // are laid end to end and cut into one contiguous range a CTA (one persistent CTA
-// an SM) -- or, where there are fewer units than CTAs, each unit into parts -- so that one
+// an SM) -- or, with fewer units than CTAs, each unit into parts -- so that one
 // long sequence fills the card; a unit cut between CTAs leaves partial results, which
 // its CTAs merge at their end, each a share of the rows.
 //
@@ -57,12 +57,21 @@ constexpr int kTreeThreads = 32 * 20;  // 5 warps a scheduler: 96 registers a th
 constexpr int kTile = 128;                 // keys a tile
 constexpr int kTilePages = kTile / kPage;  // 8
 constexpr int kGroupRows = 32;             // query rows of a softmax group
-// CTAs a unit at most, and tiles a CTA at least where there are more CTAs than units: a tile takes about 1.5 us, a merge
-// as long as 3 to 5 tiles, and longer for many pieces.
-constexpr int kMaxPieces = 40;
-#ifndef S4KV_TREE_MIN_TILES
-#define S4KV_TREE_MIN_TILES 3
-#endif
+// Where there are more CTAs than units (TreeSplit).  A part has kMinTiles tiles at least: a tile takes about 1 us, the
+// merge as long as 3 to 5.  (1 / 2 / 3 / 4: one sequence of 1000 tokens, 8 kv heads, 18.4 / 19.6 / 21.6 / 24.7 us; four of
+// 500 20.0 / 22.3 / 19.1 / 19.1; one of 300, 2 kv heads, 20.3 / 22.1 / 17.6 / 17.6; from 2000 tokens x 8 on all alike.)
+// A unit has kMaxPieces parts at most, one more for each kTilesAPiece of its tiles: a row's merge reads them all.  (One
+// unit: with 40, 40 + tiles / 16, 40 + tiles / 4 parts 22.3, 21.0, 20.9 us at 16K tokens, 34.3, 30.5, 32.0 at 64K, 82.7,
+// 45.7, 45.7 at 256K.)
+constexpr int kMinTiles = 3, kMaxPieces = 40, kTilesAPiece = 16;
+// In consecutive ranges, the beginning and end of a unit count as so many tiles.  (0 / 2 / 4 / 6 / 8: 32 sequences of 16 to
+// 8000 tokens, 8 kv heads, 152.8 / 131.7 / 122.8 / 122.8 / 124.6 us; 24 of 100 to 4000, group 8, 157.6 / 134.7 / 125.3 /
+// 114.8 / 115.9; 64 of 300 93.0 / 87.8 / 84.4 / 74.7 / 77.0; 64 of 8192 400.3 / 396.7 / 396.0 / 394.7 / 396.4.)  Parts leave
+// CTAs without work, ranges give a CTA two units to begin and end: parts are taken while the longest has no more than
+// this many tiles above an even share.  (Parts / ranges: 100 units of 1300, 3200, 5200, 10300 tokens 33.2 / 45.0,
+// 52.2 / 56.5, 74.5 / 71.8, 128.1 / 109.3 us, 1 below and 4, 9, 22 tiles above; 76 of 2200, 3200, 5200 tokens 42.0 / 45.5,
+// 51.8 / 49.5, 71.4 / 59.8, 5, 9 and 17 tiles above.)
+constexpr int kUnitTiles = 6;
 constexpr float kRefSlack = 14.0f;         // log2 slack of the softmax reference: weights up to 2^14, finite in fp16
 constexpr float kZeroUnit = 0x1p-10f;      // zero-point shares enter as share * 2^-10 (fp16) against 2^8, in units of 4
 
@@ -125,14 +134,14 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b) {
 struct TreeWalk {
   TreeSeq s;
   int b, h, rb;
-  int tile, rem;    // first tile of the current piece, tiles left from it on
-  long long start;  // flattened index of the unit's tile 0
+  int tile, rem;    // first tile of the current piece, tiles (with kUnitTiles before each further unit) left from it on
+  long long start;  // flattened index of the unit's tile 0 (ranges only)
   __device__ __forceinline__ int take() const { return min(rem, s.tiles - tile); }
   __device__ __forceinline__ int pages(int t) const { return min(kTilePages, s.L / kPage - kTilePages * (t - 1)); }
   __device__ __forceinline__ void next(const TreeParams &p) {
     const int t = take();
-    rem -= t;
-    start += s.tiles;
+    rem -= t + kUnitTiles;
+    start += s.tiles + kUnitTiles;
     tile = 0;
     if (rem <= 0) return;
     if (++rb < s.blocks) return;
@@ -154,11 +163,13 @@ static_assert(sizeof(TreeCut) == 32, "kOffCut");
 
 // How the units' tiles are dealt out.  With at least as many CTAs as units, a CTA takes a part of one unit (first ..
 // last: its unit's CTAs), so that none has two beginnings and ends; the CTAs that units leave over are shared out by
-// tiles.  With fewer, the tiles 0 .. T-1 of all units go to W CTAs in consecutive ranges, the first `extra` of `each` + 1
-// tiles, the others of `each`.
+// tiles.  With fewer CTAs, or where that would leave too much to one of them, W CTAs take consecutive ranges of all
+// units' positions, the first `extra` of `each` + 1, the others of `each` > kUnitTiles: a unit has kUnitTiles positions
+// for its beginning and end, then one a tile (so that every range has a tile).
 struct TreeSplit {
   long long each;  // 0: parts of one unit
   int extra, first, last;
+  // first position of CTA c's range, CTA of a position
   __device__ __forceinline__ long long begin(int c) const { return c * each + min(c, extra); }
   __device__ __forceinline__ int cta_of(long long x) const {
     const long long longer = extra * (each + 1);
@@ -172,7 +183,7 @@ struct TreeSplit {
   // at most ctas
   static __device__ __forceinline__ int parts(int tiles, long long T, long long units, int ctas) {
     const int c = 1 + static_cast<int>(div((ctas - units) * tiles, T));
-    return max(1, min(c, min(kMaxPieces, tiles / S4KV_TREE_MIN_TILES)));
+    return max(1, min(c, min(kMaxPieces + tiles / kTilesAPiece, tiles / kMinTiles)));
   }
 };
 
@@ -262,21 +273,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       units += static_cast<long long>(s.blocks) * H;
     }
     if (blockIdx.x == 0 && warp == 0 && bad) flag_error(p.err, bad);
-    long long T = sum;
+    long long T = sum;  // tiles
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       T += __shfl_xor_sync(kAll, T, off);
       units += __shfl_xor_sync(kAll, units, off);
     }
     if (T == 0) return;
-    const bool parts = units <= p.num_ctas;
-    // what is scanned: a sequence's CTAs or its tiles
-    auto share_of = [&](const TreeSeq &s) {
-      return static_cast<long long>(s.blocks) * H * (parts && s.tiles > 0 ? TreeSplit::parts(s.tiles, T, units, p.num_ctas) : s.tiles);
-    };
+    const long long all = T + kUnitTiles * units;  // positions
+    bool parts = units <= p.num_ctas;
     if (parts) {
-      sum = 0;
-      for (int b = b_lo; b < b_hi; ++b) sum += share_of(seq(b));
+      int longest = 0;  // part
+      for (int b = b_lo; b < b_hi; ++b) {
+        const TreeSeq s = seq(b);
+        if (s.tiles > 0) {
+          const int each = TreeSplit::parts(s.tiles, T, units, p.num_ctas);
+          longest = max(longest, (s.tiles + each - 1) / each);
+        }
+      }
+      parts = __reduce_max_sync(kAll, longest) <= kUnitTiles + TreeSplit::div(all, p.num_ctas);
+    }
+    // what is scanned: a sequence's CTAs or its positions, and a unit's
+    auto share_of = [&](const TreeSeq &s) {
+      return parts ? TreeSplit::parts(s.tiles, T, units, p.num_ctas) : s.tiles + kUnitTiles;
+    };
+    sum = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const TreeSeq s = seq(b);
+      sum += static_cast<long long>(s.blocks) * H * share_of(s);
     }
     long long incl = sum;
 #pragma unroll
@@ -284,13 +308,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       const long long t = __shfl_up_sync(kAll, incl, off);
       if (lane >= off) incl += t;
     }
-    const int W = parts ? static_cast<int>(__shfl_sync(kAll, incl, 31)) : p.num_ctas;
+    const int W = static_cast<int>(parts ? __shfl_sync(kAll, incl, 31)
+                                         : min(TreeSplit::div(all, kUnitTiles + 1), static_cast<long long>(p.num_ctas)));
     if (static_cast<int>(blockIdx.x) >= W) return;  // the whole CTA
     TreeSplit split = {0, 0, 0, 0};
     long long s0 = blockIdx.x;
+    w.rem = 0;
     if (!parts) {
-      split.each = TreeSplit::div(T, W);
-      split.extra = static_cast<int>(T - split.each * W);
+      split.each = TreeSplit::div(all, W);
+      split.extra = static_cast<int>(all - split.each * W);
       s0 = split.begin(blockIdx.x);
       w.rem = static_cast<int>(split.begin(blockIdx.x + 1) - s0);
     }
@@ -301,7 +327,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     long long pre = excl;
     if (lane == src) {
       for (bs = b_lo; bs < b_hi; ++bs) {
-        const long long mine = share_of(seq(bs));
+        const TreeSeq s = seq(bs);
+        const long long mine = static_cast<long long>(s.blocks) * H * share_of(s);
         if (s0 < pre + mine) break;
         pre += mine;
       }
@@ -309,12 +336,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     w.b = __shfl_sync(kAll, bs, src);
     pre = __shfl_sync(kAll, pre, src);
     w.s = tree_seq(p, w.b);
-    const int each = parts ? TreeSplit::parts(w.s.tiles, T, units, p.num_ctas) : w.s.tiles;
+    const int each = share_of(w.s);
     const int u = static_cast<int>(TreeSplit::div(s0 - pre, each)), k = static_cast<int>(s0 - pre - static_cast<long long>(u) * each);
     w.h = u / w.s.blocks;
     w.rb = u - w.h * w.s.blocks;
-    w.start = pre + static_cast<long long>(u) * each;
-    w.tile = k;
+    w.start = pre + static_cast<long long>(u) * each + kUnitTiles;
+    w.tile = max(0, k - kUnitTiles);
+    w.rem -= max(0, kUnitTiles - k);
     if (parts) {  // part k of the unit
       split.first = static_cast<int>(blockIdx.x) - k;
       split.last = split.first + each - 1;
@@ -1006,7 +1034,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             c.out = (static_cast<long long>(w.s.c0) * p.num_q_heads + w.h * G) * kHeadDim;
             c.first = split.each ? split.cta_of(w.start) : split.first;
             c.last = split.each ? split.cta_of(w.start + w.s.tiles - 1) : split.last;
-            c.odd = split.each && split.begin(c.first) < w.start;
+            c.odd = split.each && split.begin(c.first) < w.start - kUnitTiles;
             c.row0 = row0;
             c.rows = rows;
             c.ticket = ((w.b * H + w.h) * ((p.max_nodes * G + kTreeRows - 1) / kTreeRows) + w.rb) * 2 + g;

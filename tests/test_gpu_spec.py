@@ -252,6 +252,59 @@ def test_tree_attention_far_pages():
     assert torch.equal(out, near)
 
 
+# how the work is dealt out: lengths, nodes, kv heads, group, code width, newest nodes that may be parents
+DEALS = {
+    # fewer units than CTAs, several sequences a lane, some without nodes
+    "parts-of-many": ([(613 * i) % 3500 for i in range(45)], [(0, 1, 3, 9)[i % 4] for i in range(45)], 1, 4, 4, 2),
+    # more than half as many units as CTAs: some are cut in two, some are not
+    "parts-uneven": ([2100 - 30 * (i % 20) for i in range(50)], [2 + i % 3 for i in range(50)], 2, 2, 4, 2),
+    # nearly as many units as CTAs, one of them long: it would be one CTA's alone
+    "ranges-one-long": ([(29 * i) % 128 for i in range(70)] + [6300] + [(17 * i) % 128 for i in range(75)],
+                        [1 + i % 4 for i in range(146)], 1, 4, 4, 2),
+    "ranges-half": ([5500] * 40, [1] * 40, 2, 1, 2, 1),
+    # one unit in as many parts as there may be
+    "one-unit": ([40000], [5], 1, 4, 4, 2),
+    "int8-two-units": ([20011], [7], 2, 7, 8, 2),
+}
+
+
+@pytest.mark.parametrize("name", DEALS)
+def test_tree_attention_deals(name):
+    lens, nodes, heads, group, bits, newest = DEALS[name]
+    rng = np.random.default_rng(len(name) + sum(lens))
+    c = SpecCache(lens, heads, bits, seed=sum(nodes))
+    cu, parents, q, k, v = make_tree(rng, nodes, heads, group, c.key_scale, newest)
+    ref, bound = tree_reference(c, q, k, v, cu, parents)
+    ws = c.S.tree_workspace(q.shape[1], heads, len(nodes), max(nodes))
+    out = run_tree(c, q, k, v, cu, parents, max(nodes), ws)
+    close(out, ref, bound)
+    again = run_tree(c, q, k, v, cu, parents, max(nodes), ws)
+    assert np.array_equal(again.cpu().numpy().view(np.uint16), out.cpu().numpy().view(np.uint16))
+    assert c.S.s4kv_get_error(c.gpu) == 0
+
+
+def test_tree_attention_on_two_streams_at_once():
+    import torch
+    rng = np.random.default_rng(29)
+    both = []
+    for lens, nodes in (([5000, 33], [6, 9]), ([800] * 5, [4] * 5)):
+        c = SpecCache(lens, 2, 4, seed=len(lens))
+        cu, parents, q, k, v = make_tree(rng, nodes, 2, 4, c.key_scale, 2)
+        d = [c.dev(x) for x in (q, k, v, cu, parents)]
+        both.append((c, d, torch.zeros_like(d[0]), c.S.tree_workspace(8, 2, len(lens), max(nodes)), max(nodes),
+                     tree_reference(c, q, k, v, cu, parents)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    for _ in range(20):
+        for s, (c, d, out, ws, most, _) in zip(streams, both):
+            with torch.cuda.stream(s):
+                c.S.s4kv_tree_attention(c.gpu, *d, c.lens_dev, c.bt_dev, out, most, ws)
+    torch.cuda.synchronize()
+    for c, _, out, _, _, ref in both:
+        close(out, *ref)
+        assert c.S.s4kv_get_error(c.gpu) == 0
+
+
 def test_tree_attention_captured_and_on_another_stream():
     import torch
     rng = np.random.default_rng(19)
