@@ -95,9 +95,12 @@ constexpr uint32_t kOffFlag = kOffRed + 2 * 4 * 32 * 4;      // [2] last-piece f
 constexpr uint32_t kOffSplit = kOffFlag + 16;                  // the TreeSplit
 constexpr uint32_t kOffCut = kOffSplit + 32;                    // [2][2] the cut units' pieces, TreeCut
 constexpr uint32_t kOffOdd = kOffCut + 4 * 32;                 // [4 pieces][4 V warps] drafted values that are not finite
-constexpr uint32_t kOffBar = kOffOdd + 64;
-constexpr uint32_t kBars = 32;
+constexpr uint32_t kOffSeen = kOffOdd + 64;                     // [2][group][drafted token] the group's rows that see it
+constexpr uint32_t kOffBar = kOffSeen + 2 * 2 * 64 * 4;
+constexpr uint32_t kBars = 36;
 constexpr uint32_t kOffRing = kOffBar + 8 * kBars;
+static_assert(Fmt<4>::kVZero - Fmt<4>::kVScale == 128 && Fmt<2>::kVZero - Fmt<2>::kVScale == 128 &&
+                  Fmt<8>::kVZero - Fmt<8>::kVScale == 128, "missing pages: 256 bytes of value scales and zero points");
 static_assert(kOffQ8 % 1024 == 0 && kOffRing % 16 == 0, "operand alignment");
 
 template <int kBits>
@@ -243,9 +246,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 
   // barriers: a count of uses gives each its phase
   auto bar = [&](int i) { return base + kOffBar + 8u * i; };
-  auto full = [&](int s) { return bar(s); };        // page stages
-  auto empty = [&](int s) { return bar(6 + s); };
-  auto k_ready = [&](int x) { return bar(12 + x); };  // K and the zero-point operand written
+  auto full = [&](int s) { return bar(s); };          // page stages: the page warp and its copies
+  auto empty = [&](int s) { return bar(6 + s); };     // (10: K, V and helper warps)
+  auto k_ready = [&](int x) { return bar(12 + x); };  // K and the zero-point operand written (6: K and helper warps)
   auto k_free = [&](int x) { return bar(14 + x); };
   auto v_ready = [&](int x) { return bar(16 + x); };
   auto v_free = [&](int x) { return bar(18 + x); };
@@ -255,17 +258,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   auto p_free = [&](int x) { return bar(26 + x); };
   auto q_full = [&](int x) { return bar(28 + x); };
   auto q_free = [&](int x) { return bar(30 + x); };
+  auto seen_full = [&](int x) { return bar(32 + x); };
+  auto seen_free = [&](int x) { return bar(34 + x); };
+
+  // ---- barriers and the one-hot operand, while the plan's first loads come
+  const int per = (B + 31) >> 5, b_lo = min(B, lane * per), b_hi = min(B, b_lo + per);
+  // (a batch of up to 32 has one sequence a lane, read once)
+  const TreeSeq mine0 = tree_seq(p, min(b_lo, B - 1));
+  if (warp == 0) {
+    for (int i = lane; i < static_cast<int>(kBars); i += 32) {
+      // their arrivals, 4 bits a barrier
+      const unsigned long long counts = i < 16 ? 0x1166AAAAAA111111ull : i < 32 ? 0x1122118818111144ull : 0x8811ull;
+      mbar_init(bar(i), static_cast<uint32_t>(counts >> (4 * (i & 15))) & 15u);
+    }
+    if (lane == 0) *abort_flag = 0;
+    fence_barrier_init();
+  }
+  // the one-hot operand: token t counts the shares (hi and lo) of page t / 16, times 2^8
+#pragma unroll 1
+  for (int i = tid; i < kTile * 8; i += kTreeThreads) {
+    const int t = i >> 3, k = 2 * (i & 7);
+    uint32_t v = 0;
+    if ((k & 7) == (t / kPage & ~1)) v = (t / kPage & 1) ? 0x5C000000u : 0x00005C00u;
+    sts32(base + kOffHot + tc05::plain16_offset(t, k), v);
+  }
 
   // ---- plan: every warp finds this CTA's range for itself
   TreeWalk w;
   {
-    const int per = (B + 31) >> 5;
-    const int b_lo = min(B, lane * per), b_hi = min(B, b_lo + per);
     long long sum = 0, units = 0;
     uint32_t bad = 0;
-    // (a batch of up to 32 has one sequence a lane, read once)
-    const TreeSeq mine0 = tree_seq(p, min(b_lo, B - 1));
     auto seq = [&](int b) { return b == b_lo ? mine0 : tree_seq(p, b); };
+#pragma unroll 1
     for (int b = b_lo; b < b_hi; ++b) {
       const TreeSeq s = seq(b);
       bad |= s.bad;
@@ -284,6 +308,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     bool parts = units <= p.num_ctas;
     if (parts) {
       int longest = 0;  // part
+#pragma unroll 1
       for (int b = b_lo; b < b_hi; ++b) {
         const TreeSeq s = seq(b);
         if (s.tiles > 0) {
@@ -298,6 +323,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       return parts ? TreeSplit::parts(s.tiles, T, units, p.num_ctas) : s.tiles + kUnitTiles;
     };
     sum = 0;
+#pragma unroll 1
     for (int b = b_lo; b < b_hi; ++b) {
       const TreeSeq s = seq(b);
       sum += static_cast<long long>(s.blocks) * H * share_of(s);
@@ -326,6 +352,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     int bs = 0;
     long long pre = excl;
     if (lane == src) {
+#pragma unroll 1
       for (bs = b_lo; bs < b_hi; ++bs) {
         const TreeSeq s = seq(bs);
         const long long mine = static_cast<long long>(s.blocks) * H * share_of(s);
@@ -358,35 +385,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     tc05::tmem_relinquish();
     tc05::fence_before_sync();
   }
-  if (tid == 0) {
-    for (int s = 0; s < R::kStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 10);  // K, V and helper warps
-    }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(k_ready(x), 6);  // K and helper warps
-      mbar_init(k_free(x), 1);
-      mbar_init(v_ready(x), 4);
-      mbar_init(v_free(x), 1);
-      mbar_init(p_full(x), 8);
-      mbar_init(p_free(x), 1);
-      mbar_init(q_full(x), 2);
-      mbar_init(q_free(x), 1);
-    }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, 8);
-    mbar_init(merged(0), 1);
-    mbar_init(merged(1), 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  // the one-hot operand: token t counts the shares (hi and lo) of page t / 16, times 2^8
-  for (int i = tid; i < kTile * 8; i += kTreeThreads) {
-    const int t = i >> 3, k = 2 * (i & 7);
-    uint32_t v = 0;
-    if ((k & 7) == (t / kPage & ~1)) v = (t / kPage & 1) ? 0x5C000000u : 0x00005C00u;
-    sts32(base + kOffHot + tc05::plain16_offset(t, k), v);
-  }
   fence_proxy_async();
   __syncthreads();
   tc05::fence_after_sync();
@@ -402,23 +400,99 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 
   if (warp == kPageWarp) {
     // ------------------------------------------------- pages into the ring
-    int k = 0;  // stages filled
+    // and who sees whom: the rows of either group that see a drafted token
+    auto see = [&](int su, int (&up)[2]) {
+      const int n = w.s.n;
+      if (su >= 2 && !wait_warp(seen_free(su & 1), prev2(su))) return false;
+      // ancestors of nodes lane and lane + 32, themselves among them, by pointer doubling
+      unsigned long long anc[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int a = lane + 32 * e;
+        if (up[e] < -1 || up[e] >= a) {
+          if (a < n) flag_error(p.err, S4KV_EFLAG_TREE);
+          up[e] = -1;
+        }
+        anc[e] = 1ull << a;
+      }
+#pragma unroll 1
+      for (int s = 1; s < n; s <<= 1) {
+        unsigned long long m[2];
+        int u[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const unsigned long long m0 = __shfl_sync(kAll, anc[0], up[e] & 31), m1 = __shfl_sync(kAll, anc[1], up[e] & 31);
+          const int u0 = __shfl_sync(kAll, up[0], up[e] & 31), u1 = __shfl_sync(kAll, up[1], up[e] & 31);
+          m[e] = up[e] < 0 ? 0ull : up[e] < 32 ? m0 : m1;
+          u[e] = up[e] < 0 ? -1 : up[e] < 32 ? u0 : u1;
+        }
+        anc[0] |= m[0];
+        anc[1] |= m[1];
+        up[0] = u[0];
+        up[1] = u[1];
+        if (!__any_sync(kAll, up[0] >= 0 || up[1] >= 0)) break;
+      }
+      // turned round, node by node: its rows (of all 64) see the tokens lane and lane + 32 if these are among its ancestors;
+      // rows that the unit does not have see token 0, so that their sums are finite
+      const int first = kTreeRows * w.rb, rows = min(kTreeRows, n * G - first);
+      unsigned long long seen[2] = {lane == 0 && rows < kTreeRows ? ~0ull << rows : 0ull, 0ull};
+#pragma unroll 1
+      for (int node = first / G; node * G < first + rows; ++node) {
+        const unsigned long long m = node < 32 ? __shfl_sync(kAll, anc[0], node) : __shfl_sync(kAll, anc[1], node - 32);
+        const int from = max(node * G - first, 0), to = min(node * G + G - first, rows);  // 0 <= from < to <= 64
+        const unsigned long long mine = ~0ull >> (64 - (to - from)) << from;
+        if (m >> lane & 1) seen[0] |= mine;
+        if (m >> (lane + 32) & 1) seen[1] |= mine;
+      }
+      const uint32_t at = base + kOffSeen + 4 * (128 * (su & 1) + lane);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sts32(at + 128 * e, static_cast<uint32_t>(seen[e]));
+        sts32(at + 128 * e + 256, static_cast<uint32_t>(seen[e] >> 32));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(seen_full(su & 1));
+      return true;
+    };
+    int k = 0, su = 0;  // stages filled, pieces with a tile 0
     while (w.rem > 0 && !failed) {
       const int t1 = w.tile + w.take();
       const int32_t *bt = p.block_tables + static_cast<long>(w.b) * p.max_pages;
       const uint8_t *head = p.pool + static_cast<long long>(w.h) * F::kBlock;
       const int t0 = max(w.tile, 1);
-      // the ids of a tile are read while the stage of the tile before is waited for
-      int id = 0;
-      if (t0 < t1 && lane < w.pages(t0)) id = __ldg(bt + kTilePages * (t0 - 1) + lane);
-      for (int t = t0; t < t1; ++t, ++k) {
+      // masks are made while the ring is full, but the first piece's behind the copies of its first pages
+      const int t_see = w.tile > 0 ? t1 + 1 : k > 0 ? t0 : min(t0 + 1, t1);
+      // the ids of 4 tiles are read at once, before the 4 tiles ahead of them are fetched
+      const int last = min(w.s.L / kPage, kTilePages * (t1 - 1));
+      auto ids_of = [&](int t) { return kTilePages * (t - 1) + lane < last ? __ldg(bt + kTilePages * (t - 1) + lane) : 0; };
+      int ids = t0 < t1 ? ids_of(t0) : 0, ids_next = t0 + 4 < t1 ? ids_of(t0 + 4) : 0;
+      int up[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        up[e] = w.tile == 0 && lane + 32 * e < w.s.n ? __ldg(p.parents + w.s.c0 + lane + 32 * e) : -1;
+#pragma unroll 1
+      for (int t = t0;; ++t, ++k) {
+        if (t == t_see && !see(su++, up)) {
+          fail();
+          break;
+        }
+        if (t >= t1) break;
         const int np = w.pages(t), st = k % R::kStages;
-        int phys = id;
-        if (t + 1 < t1 && lane < w.pages(t + 1)) id = __ldg(bt + kTilePages * t + lane);
+        int phys = __shfl_sync(kAll, ids, (kTilePages * (t - t0) + lane) & 31);
+        if (((t - t0) & 3) == 3) {
+          ids = ids_next;
+          ids_next = t + 5 < t1 ? ids_of(t + 5) : 0;
+        }
         if (k >= R::kStages && !wait_warp(empty(st), (k / R::kStages - 1) & 1)) {
           fail();
           break;
         }
+        // missing pages: value = code * 0 + 0, which a weight of 0 leaves alone (what the stage held might not be finite)
+#pragma unroll 1
+        for (int y = 16 * np + lane; y < 16 * kTilePages; y += 32)
+          sts128(base + kOffRing + st * R::kStage + (y >> 4) * R::kPageStride + F::kVScale + 16 * (y & 15), make_uint4(0, 0, 0, 0));
+        if (np < kTilePages) fence_proxy_async();
+        __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(full(st), np * F::kBlock);
         __syncwarp();
         if (lane < np) {
@@ -526,7 +600,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
               }
             }
           } else if (is_v) {
-            // pages in batches of 4; lanes 0-15 of the quarter: channels 32 wq + 4n + {0, 1}, 16-31: + {2, 3}
+            // pages in batches of 4 (missing ones have scale and zero point 0); lanes 0-15 of the quarter: channels 32 wq + 4n + {0, 1}, 16-31: + {2, 3}
             const uint32_t sv = stage + F::kVScale + 32 * i + 4 * wq, zv = stage + F::kVZero + 32 * wq + 4 * i;
             const uint32_t cv = stage + F::kVCode + (kBits == 8 ? 512 * wq + 16 * lane
                                                      : kBits == 4 ? 512 * (wq >> 1) + 16 * lane + 8 * (wq & 1) : 16 * lane + 4 * wq);
@@ -560,16 +634,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 #pragma unroll 1
             for (int pb = 0; pb < kTilePages; pb += 4) {
               uint32_t o0[16], o1[16];
-              if (pb + 4 <= np) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) page(pb + j, o0 + 4 * j, o1 + 4 * j);
-              } else {  // missing pages are zeros: their weights are 0, and 0 * what the stage held need not be
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o0[j] = o1[j] = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (pb + j < np) page(pb + j, o0 + 4 * j, o1 + 4 * j);
-              }
+              for (int j = 0; j < 4; ++j) page(pb + j, o0 + 4 * j, o1 + 4 * j);
               tc05::tmem_st_frag16(tV + lane_base + 8 * pb, o0);
               tc05::tmem_st_frag16(tV + lane_base + (16u << 16) + 8 * pb, o1);
             }
@@ -645,30 +711,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
               return x;
             };
 #pragma unroll 1
-            for (int pb = 0; pb < kTilePages; pb += 4) {
-              uint32_t o0[16], o1[16];
+            for (int pg = 0; pg < kTilePages; ++pg) {
+              int count;
+              long stride;
+              const __half *rv = rows_of(pg, p.v, p.res_v, count, stride) + 32 * wq + 4 * n;
+              uint2 x[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                int count;
-                long stride;
-                const __half *rv = rows_of(pb + j, p.v, p.res_v, count, stride);
-                uint2 x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int tk = 2 * i + (e & 1) + 8 * (e >> 1);
-                  x[e] = tk < count ? *reinterpret_cast<const uint2 *>(rv + tk * stride + 32 * wq + 4 * n) : make_uint2(0, 0);
-                  if (pb == 0) x[e] = make_uint2(finite(x[e].x), finite(x[e].y));
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  o0[4 * j + 2 * e] = __byte_perm(x[2 * e].x, x[2 * e + 1].x, 0x5410);
-                  o0[4 * j + 2 * e + 1] = __byte_perm(x[2 * e].x, x[2 * e + 1].x, 0x7632);
-                  o1[4 * j + 2 * e] = __byte_perm(x[2 * e].y, x[2 * e + 1].y, 0x5410);
-                  o1[4 * j + 2 * e + 1] = __byte_perm(x[2 * e].y, x[2 * e + 1].y, 0x7632);
-                }
+              for (int e = 0; e < 4; ++e) {
+                const int tk = 2 * i + (e & 1) + 8 * (e >> 1);
+                x[e] = tk < count ? *reinterpret_cast<const uint2 *>(rv + tk * stride) : make_uint2(0, 0);
+                if (pg < 4) x[e] = make_uint2(finite(x[e].x), finite(x[e].y));
               }
-              tc05::tmem_st_frag16(tV + lane_base + 8 * pb, o0);
-              tc05::tmem_st_frag16(tV + lane_base + (16u << 16) + 8 * pb, o1);
+              uint32_t o0[4], o1[4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                o0[2 * e] = __byte_perm(x[2 * e].x, x[2 * e + 1].x, 0x5410);
+                o0[2 * e + 1] = __byte_perm(x[2 * e].x, x[2 * e + 1].x, 0x7632);
+                o1[2 * e] = __byte_perm(x[2 * e].y, x[2 * e + 1].y, 0x5410);
+                o1[2 * e + 1] = __byte_perm(x[2 * e].y, x[2 * e + 1].y, 0x7632);
+              }
+              tc05::tmem_st_frag4(tV + lane_base + 8 * pg, o0);
+              tc05::tmem_st_frag4(tV + lane_base + (16u << 16) + 8 * pg, o1);
             }
             odd = __any_sync(kAll, odd);
             if (lane == 0) reinterpret_cast<volatile int *>(sm + kOffOdd)[4 * (uc & 3) + wq] = odd;
@@ -727,17 +790,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       tc05::fence_after_sync();
       const uint64_t dp = tc05::smem_desc_mn64(base + kOffP + (2 * x2) * kPBytes, kPBytes);
       const uint32_t tV = tmem + kTmV + 64u * x2;
+      if (tc05::elect_one()) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        tc05::mma_f16_ts(tmem + kTmO, tV + 8 * j, dp + ((2048 * j) >> 4), kIdescTO, (!fresh || j > 0) ? 1u : 0u);
-      tc05::mma_commit(p_free(x2));
-      tc05::mma_commit(v_free(x2));
+        for (int j = 0; j < 8; ++j)
+          tc05::issue_f16_ts(tmem + kTmO, tV + 8 * j, dp + ((2048 * j) >> 4), kIdescTO, (!fresh || j > 0) ? 1u : 0u);
+        tc05::issue_commit(p_free(x2));
+        tc05::issue_commit(v_free(x2));
+      }
+      __syncwarp();
       return true;
     };
     while (w.rem > 0 && !failed) {
       const int t1 = w.tile + w.take();
       const uint64_t dq = tc05::smem_desc_sw128(base + kOffQHi + (uc & 1) * kQHiBytes);
       const uint64_t dq8 = tc05::smem_desc_sw128(base + kOffQ8 + (uc & 1) * kQ8Bytes);
+      // the last product of the piece before first: its sums wait for it, and nobody yet for this piece's logits
       for (int t = w.tile; t < t1; ++t, ++kt) {
         const int x2 = kt & 1;
         if ((t == w.tile && !wait_warp(q_full(uc & 1), (uc >> 1) & 1)) || !wait_warp(k_ready(x2), (kt >> 1) & 1) ||
@@ -747,17 +814,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         }
         tc05::fence_after_sync();
         const uint32_t tS = tmem + kTmS, tKhi = tmem + kTmKhi + 64u * x2, tKlo = tmem + kTmKlo + 32u * x2;
+        if (tc05::elect_one()) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          tc05::mma_f16_ts(tS, tKhi + 8 * j, dq + (((j >> 2) * (kQHiBytes / 2) + (j & 3) * 32) >> 4), kIdescTS, j > 0 ? 1u : 0u);
-        if (t > 0) {
+          for (int j = 0; j < 8; ++j)
+            tc05::issue_f16_ts(tS, tKhi + 8 * j, dq + (((j >> 2) * (kQHiBytes / 2) + (j & 3) * 32) >> 4), kIdescTS, j > 0 ? 1u : 0u);
+          if (t > 0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tc05::mma_e5m2_ts(tS, tKlo + 8 * j, dq8 + ((32 * j) >> 4), kIdescTS8, 1u);
-          tc05::mma_f16_ss(tS, dhot, tc05::smem_desc_plain16(base + kOffZero + x2 * (kTreeRows * 32)), kIdescTS, 1u);
+            for (int j = 0; j < 4; ++j) tc05::issue_e5m2_ts(tS, tKlo + 8 * j, dq8 + ((32 * j) >> 4), kIdescTS8, 1u);
+            tc05::issue_f16_ss(tS, dhot, tc05::smem_desc_plain16(base + kOffZero + x2 * (kTreeRows * 32)), kIdescTS, 1u);
+          }
+          tc05::issue_commit(s_full);
+          tc05::issue_commit(k_free(x2));
+          if (t + 1 == t1) tc05::issue_commit(q_free(uc & 1));
         }
-        tc05::mma_commit(s_full);
-        tc05::mma_commit(k_free(x2));
-        if (t + 1 == t1) tc05::mma_commit(q_free(uc & 1));
+        __syncwarp();
         if (kt > 0 && !issue_pv(kt - 1)) {
           fail();
           break;
@@ -781,7 +851,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     bool ok = true;  // the group leaves together: a failed wait is told at the next vote
     TreeCut *cuts = reinterpret_cast<TreeCut *>(sm + kOffCut) + 2 * g;
     bool first_piece = true;
-    int kt = 0, uc = 0, num_cuts = 0, merges = 0;
+    int kt = 0, uc = 0, su = 0, num_cuts = 0, merges = 0;  // (su: pieces with a tile 0)
     while (w.rem > 0 && !failed) {
       const int t0 = w.tile, t1 = w.tile + w.take();
       const int rows = min(kGroupRows, w.s.n * G - kTreeRows * w.rb - kGroupRows * g);  // of this group
@@ -794,62 +864,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         group_sync(bid);
       }
       uint32_t seen = 0;  // tile 0: the rows that see this token
-      if (t0 == 0 && rows > 0) {
-        if (wq < 2) {
-          // ancestors of nodes lane and lane + 32, themselves among them, by pointer doubling
-          int up[2];
-          unsigned long long anc[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int a = lane + 32 * e;
-            up[e] = a < w.s.n ? __ldg(p.parents + w.s.c0 + a) : -1;
-            if (up[e] < -1 || up[e] >= a) {
-              if (a < w.s.n) flag_error(p.err, S4KV_EFLAG_TREE);
-              up[e] = -1;
-            }
-            anc[e] = 1ull << a;
-          }
-#pragma unroll 1
-          for (int s = 1; s < w.s.n; s <<= 1) {
-            unsigned long long m[2];
-            int u[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const unsigned long long m0 = __shfl_sync(kAll, anc[0], up[e] & 31), m1 = __shfl_sync(kAll, anc[1], up[e] & 31);
-              const int u0 = __shfl_sync(kAll, up[0], up[e] & 31), u1 = __shfl_sync(kAll, up[1], up[e] & 31);
-              m[e] = up[e] < 0 ? 0ull : up[e] < 32 ? m0 : m1;
-              u[e] = up[e] < 0 ? -1 : up[e] < 32 ? u0 : u1;
-            }
-            anc[0] |= m[0];
-            anc[1] |= m[1];
-            up[0] = u[0];
-            up[1] = u[1];
-          }
-          // transposed: the nodes that have token 32 wq + lane among them
-          const uint32_t a0 = static_cast<uint32_t>(anc[0] >> (32 * wq)), a1 = static_cast<uint32_t>(anc[1] >> (32 * wq));
-          uint32_t d0 = 0, d1 = 0;
-#pragma unroll 4
-          for (int j = 0; j < 32; ++j) {
-            const uint32_t b0 = __ballot_sync(kAll, a0 >> j & 1), b1 = __ballot_sync(kAll, a1 >> j & 1);
-            if (lane == j) {
-              d0 = b0;
-              d1 = b1;
-            }
-          }
-          // and from nodes to rows; rows that the unit does not have see token 0, so that their sums are finite
-          int node = (kTreeRows * w.rb + kGroupRows * g) / G, head = kTreeRows * w.rb + kGroupRows * g - node * G;
-#pragma unroll 4
-          for (int j = 0; j < 32; ++j) {
-            const uint32_t s = j < rows ? (node < 32 ? d0 >> node : d1 >> (node - 32)) : (tl == 0 ? 1u : 0u);
-            seen |= (s & 1u) << j;
-            if (++head == G) {
-              head = 0;
-              ++node;
-            }
-          }
-        } else {
+      if (t0 == 0) {
+        if (rows > 0 && wq < 2) {
+          ok = ok && wait_warp(seen_full(su & 1), (su >> 1) & 1);
+          seen = lds32_at(base + kOffSeen + 4 * (64 * (2 * (su & 1) + g) + tl));
+        } else if (wq >= 2) {
           seen = tl - 64 < w.s.L % kPage ? 0xFFFFFFFFu : 0u;  // the residual rows
         }
+        __syncwarp();
+        ++su;
       }
       for (int t = t0; t < t1; ++t, ++kt) {
         const int x2 = kt & 1;
@@ -858,6 +881,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           ok = ok && (kt < 2 || wait_warp(p_free(x2), prev2(kt)));
           if (!ok) *abort_flag = 1;  // the group leaves at its next vote
           if (lane == 0) {
+            if (t == 0) mbar_arrive(seen_free((su - 1) & 1));
             mbar_arrive(s_free);
             mbar_arrive(p_full(x2));
           }
@@ -935,7 +959,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         // S has been read
         tc05::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
+        if (lane == 0) {
+          if (t == 0) mbar_arrive(seen_free((su - 1) & 1));
+          mbar_arrive(s_free);
+        }
         ok = ok && (kt < 2 || wait_warp(p_free(x2), prev2(kt)));
         const uint32_t ph = base + kOffP + (2 * x2) * kPBytes + (tl >> 3) * 1024 + (tl & 7) * 128;
 #pragma unroll
@@ -973,20 +1000,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         }
         const float lsum = red[lane] + red[32 + lane] + red[64 + lane] + red[96 + lane];
         tc05::fence_after_sync();
-        float o[32];
-        {
-          float lo[32];
-          tc05::tmem_ld32(tO, reinterpret_cast<uint32_t (&)[32]>(o));
-          tc05::tmem_ld32(tO + kTreeRows, reinterpret_cast<uint32_t (&)[32]>(lo));
-          tc05::tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] += lo[j];
-        }
         const int row0 = kTreeRows * w.rb + kGroupRows * g;
-        const int ch = 32 * wq + 4 * (lane & 7) + 2 * (lane >> 4) + (lane >> 3 & 1);  // the channel of this lane
-        if (t0 == 0 && reinterpret_cast<volatile int *>(sm + kOffOdd)[4 * (uc & 3) + wq]) {
-          // drafted values that are not finite, to the rows that see them: +infinity in `more`, -infinity in `less`, NaN in both
-          uint32_t more = 0, less = 0;
+        const int ch = 32 * wq + 4 * (lane & 7) + 2 * (lane >> 4) + (lane >> 3 & 1);
+        // drafted values that are not finite, to the rows that see them: +infinity in `more`, -infinity in `less`, NaN in both
+        uint32_t more = 0, less = 0;
+        if (t0 == 0 && *(reinterpret_cast<volatile int *>(sm + kOffOdd) + 4 * (uc & 3) + wq)) {
 #pragma unroll 1
           for (int j = 0; j < rows; ++j)
             for (int a = (row0 + j) / G; a >= 0;) {
@@ -996,35 +1014,47 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
               const int up = __ldg(p.parents + w.s.c0 + a);
               a = up < a ? up : -1;
             }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (more >> j & 1) o[j] += INFINITY;
-            if (less >> j & 1) o[j] -= INFINITY;
-          }
         }
-        // out of row j = o[j] times lane j's factor
-        auto store = [&](float factor) {
-          int head = row0 % G;
-          __half *dst = p.out + (static_cast<long>(w.s.c0 + row0 / G) * p.num_q_heads + w.h * G + head) * kHeadDim + ch;
+        // 8 rows at a time (the loop is short: a unit's end is run once in a while, and would be fetched each time)
+        const bool whole = t0 == 0 && t1 == w.s.tiles;
+        const long long slot = 2ll * blockIdx.x + (first_piece ? 0 : 1);
+        const float factor = 1.0f / lsum;
+        int head = row0 % G;
+        __half *dst = p.out + (static_cast<long>(w.s.c0 + row0 / G) * p.num_q_heads + w.h * G + head) * kHeadDim + ch;
+        float *part = p.part + (slot * kTreeRows + kGroupRows * g) * kHeadDim + ch;
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 8) {
+          float o[8], lo[8];
+          tc05::tmem_ld8(tO + c, o);
+          tc05::tmem_ld8(tO + kTreeRows + c, lo);
+          tc05::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const __half x = __float2half_rn(o[j] * __shfl_sync(kAll, factor, j));
-            if (j < rows) *dst = x;
-            dst += kHeadDim;
-            if (++head == G) {
-              head = 0;
-              dst += static_cast<long>(p.num_q_heads - G) * kHeadDim;
+          for (int j = 0; j < 8; ++j) o[j] += lo[j];
+          if (__any_sync(kAll, (more | less) != 0)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (more >> (c + j) & 1) o[j] += INFINITY;
+              if (less >> (c + j) & 1) o[j] -= INFINITY;
             }
           }
-        };
-        if (t0 == 0 && t1 == w.s.tiles) {
-          store(1.0f / lsum);
-        } else {
-          const long long slot = 2ll * blockIdx.x + (first_piece ? 0 : 1);
-          float *dst = p.part + (slot * kTreeRows + kGroupRows * g) * kHeadDim + ch;
+          if (whole) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < rows) dst[j * kHeadDim] = o[j];
+            for (int j = 0; j < 8; ++j) {
+              const __half x = __float2half_rn(o[j] * __shfl_sync(kAll, factor, c + j));
+              if (c + j < rows) *dst = x;
+              dst += kHeadDim;
+              if (++head == G) {
+                head = 0;
+                dst += static_cast<long>(p.num_q_heads - G) * kHeadDim;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (c + j < rows) part[(c + j) * kHeadDim] = o[j];
+          }
+        }
+        if (!whole) {
           if (wq == 0) p.part_ml[slot * kTreeRows + kGroupRows * g + lane] = make_float2(myref, lsum);
           __threadfence();
           group_sync(bid);
