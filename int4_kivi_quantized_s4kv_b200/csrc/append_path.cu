@@ -8,6 +8,12 @@
 // Grid: (page slot, sequence, kv head), 128 threads, as in s4kv_append: slot s
 // takes the s-th page that the path touches, and slot 0 writes the partial tail
 // after it has read the residual rows that its own page needed.
+//
+// Bound by latency: a chain of launch, lengths and path, rows, quantization, and a
+// few KB a CTA.  The lengths, the path, the page's id and the residual rows are
+// therefore fetched at once.  Measured, captured and warm, followed by s4kv_dequant_pages
+// of the cache: one sequence's path of up to 4 nodes, 8 kv heads, 6.5 us; 128
+// sequences' paths of up to 8 18 us.
 #include "kernels.cuh"
 #include "quant.cuh"
 

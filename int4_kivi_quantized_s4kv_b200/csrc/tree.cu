@@ -38,8 +38,14 @@
 // weight would pass 2^14 (still finite in fp16): a vote of the group decides, and
 // moving it (a maximum over the 128 tokens, the sums and O rescaled) is rare.
 //
-// Bound by HBM when R = nodes x G is small (176 bytes of int4 cache a token feed 512 R
-// operations), by the MMAs and the shared-memory port for many rows.
+// What bounds it: 176 bytes of int4 cache a token feed 512 R operations (R = nodes x G), so that HBM would for few rows
+// and the tensor pipe for many; in fact it is the warps' instruction issue (about 8300 warp instructions a tile: softmax
+// 2800, keys 1850, values 1270, the rest waiting and issuing; 62% of the issue slots) and the chain S, softmax, O, which
+// one set of accumulators leaves no second of.  Measured: 64 sequences of 8192 tokens, 16 nodes, group 4: 394 us, 1.9 TB/s
+// of cache, 0.35 PFLOP/s; 8 of 32768, 64 nodes, group 8: 1400 to 1600 us with the clock, 0.35 to 0.39 PFLOP/s; one of
+// 32768: 44 us; two of 16 tokens: 12.3 us.  For short contexts a unit's beginning and end count for more than its tiles,
+// and the code that they alone run is fetched each time (5 of 20 warps wait for instructions with 300 tokens a sequence),
+// so that it is kept small: rolled loops, one copy.
 #include <cfloat>
 #include <type_traits>
 
@@ -57,20 +63,18 @@ constexpr int kTreeThreads = 32 * 20;  // 5 warps a scheduler: 96 registers a th
 constexpr int kTile = 128;                 // keys a tile
 constexpr int kTilePages = kTile / kPage;  // 8
 constexpr int kGroupRows = 32;             // query rows of a softmax group
-// Where there are more CTAs than units (TreeSplit).  A part has kMinTiles tiles at least: a tile takes about 1 us, the
-// merge as long as 3 to 5.  (1 / 2 / 3 / 4: one sequence of 1000 tokens, 8 kv heads, 18.4 / 19.6 / 21.6 / 24.7 us; four of
-// 500 20.0 / 22.3 / 19.1 / 19.1; one of 300, 2 kv heads, 20.3 / 22.1 / 17.6 / 17.6; from 2000 tokens x 8 on all alike.)
+// Where there are more CTAs than units (TreeSplit).  A part has kMinTiles tiles at least: a tile takes 1 to 2 us, the
+// merge as long as a few.  (1 / 2 / 3 / 4: one sequence of 1000 tokens, 8 kv heads, 18.7 / 20.4 / 20.8 / 24.0 us; four of
+// 500 20.4 / 22.8 / 20.0 / 19.9; one of 300, 2 kv heads, 18.5 / 20.4 / 17.7 / 17.7; from 2000 tokens x 8 on all alike.)
 // A unit has kMaxPieces parts at most, one more for each kTilesAPiece of its tiles: a row's merge reads them all.  (One
-// unit: with 40, 40 + tiles / 16, 40 + tiles / 4 parts 22.3, 21.0, 20.9 us at 16K tokens, 34.3, 30.5, 32.0 at 64K, 82.7,
-// 45.7, 45.7 at 256K.)
+// unit: with 40, 40 + tiles / 16, 40 + tiles / 4 parts 23.0, 21.6, 21.6 us at 16K tokens, 27.0, 25.2, 26.7 at 32K.)
 constexpr int kMinTiles = 3, kMaxPieces = 40, kTilesAPiece = 16;
-// In consecutive ranges, the beginning and end of a unit count as so many tiles.  (0 / 2 / 4 / 6 / 8: 32 sequences of 16 to
-// 8000 tokens, 8 kv heads, 152.8 / 131.7 / 122.8 / 122.8 / 124.6 us; 24 of 100 to 4000, group 8, 157.6 / 134.7 / 125.3 /
-// 114.8 / 115.9; 64 of 300 93.0 / 87.8 / 84.4 / 74.7 / 77.0; 64 of 8192 400.3 / 396.7 / 396.0 / 394.7 / 396.4.)  Parts leave
-// CTAs without work, ranges give a CTA two units to begin and end: parts are taken while the longest has no more than
-// this many tiles above an even share.  (Parts / ranges: 100 units of 1300, 3200, 5200, 10300 tokens 33.2 / 45.0,
-// 52.2 / 56.5, 74.5 / 71.8, 128.1 / 109.3 us, 1 below and 4, 9, 22 tiles above; 76 of 2200, 3200, 5200 tokens 42.0 / 45.5,
-// 51.8 / 49.5, 71.4 / 59.8, 5, 9 and 17 tiles above.)
+// In consecutive ranges, the beginning and end of a unit count as so many tiles.  (3 / 4 / 6 / 8: 128 sequences of 16 to
+// 2000 tokens, 8 kv heads, 202.3 / 196.3 / 191.3 / 181.4 us; 64 of 300 67.7 / 65.7 / 61.3 / 63.0; 24 of 100 to 4000, group
+// 8, 107.7 / 104.6 / 108.0 / 112.7; 64 of 8192 all alike; with 0 a third more on an earlier state.)  Parts leave CTAs
+// without work, ranges give a CTA two units to begin and end: parts are taken while the longest has no more than this
+// many tiles above an even share.  (Parts / ranges: 100 units of 2048, 5120, 10240 tokens 42.7 / 50.0, 75.0 / 71.8,
+// 129.1 / 108.2 us, 2, 9 and 22 tiles above; 76 of them 41.7 / 42.0, 71.5 / 59.3, 128.6 / 90.1, 5, 17 and 36 above.)
 constexpr int kUnitTiles = 6;
 constexpr float kRefSlack = 14.0f;         // log2 slack of the softmax reference: weights up to 2^14, finite in fp16
 constexpr float kZeroUnit = 0x1p-10f;      // zero-point shares enter as share * 2^-10 (fp16) against 2^8, in units of 4
