@@ -186,11 +186,11 @@ struct TreeSplit {
   static __device__ __forceinline__ long long div(long long x, long long y) {
     return ((x | y) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
   }
-  // CTAs of a unit of `tiles` tiles where T tiles in `units` units meet `ctas` >= units CTAs: all units' together are
-  // at most ctas
-  static __device__ __forceinline__ int parts(int tiles, long long T, long long units, int ctas) {
-    const int c = 1 + static_cast<int>(div((ctas - units) * tiles, T));
-    return max(1, min(c, min(kMaxPieces + tiles / kTilesAPiece, tiles / kMinTiles)));
+  // CTAs of a unit of `tiles` tiles; `spare` = (CTAs - units) / tiles of all units, less 2^-20 of it for the roundings, so
+  // that all units' together are no more than there are
+  static __device__ __forceinline__ int parts(int tiles, float spare) {
+    const uint32_t t = tiles, c = 1 + static_cast<uint32_t>(static_cast<float>(t) * spare);
+    return max(1u, min(c, min(kMaxPieces + t / kTilesAPiece, t / kMinTiles)));
   }
 };
 
@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   // ---- plan: every warp finds this CTA's range for itself
   TreeWalk w;
   {
-    long long sum = 0, units = 0;
+    long long sum = 0;
+    uint32_t units = 0;  // at most 2^30
     uint32_t bad = 0;
     auto seq = [&](int b) { return b == b_lo ? mine0 : tree_seq(p, b); };
 #pragma unroll 1
@@ -298,33 +299,30 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       const TreeSeq s = seq(b);
       bad |= s.bad;
       sum += static_cast<long long>(s.tiles) * s.blocks * H;
-      units += static_cast<long long>(s.blocks) * H;
+      units += s.blocks * H;
     }
     if (blockIdx.x == 0 && warp == 0 && bad) flag_error(p.err, bad);
-    long long T = sum;  // tiles
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      T += __shfl_xor_sync(kAll, T, off);
-      units += __shfl_xor_sync(kAll, units, off);
-    }
+    units = __reduce_add_sync(kAll, units);
+    // tiles, at most 2^24 a unit
+    const long long T = (static_cast<long long>(__reduce_add_sync(kAll, static_cast<uint32_t>(sum >> 24))) << 24) +
+                        __reduce_add_sync(kAll, static_cast<uint32_t>(sum) & 0xFFFFFFu);
     if (T == 0) return;
-    const long long all = T + kUnitTiles * units;  // positions
-    bool parts = units <= p.num_ctas;
+    const long long all = T + static_cast<long long>(kUnitTiles) * units;  // positions
+    const long long even = TreeSplit::div(all, p.num_ctas);
+    bool parts = units <= static_cast<uint32_t>(p.num_ctas);
+    const float spare = __fdividef(static_cast<float>(p.num_ctas - static_cast<int>(units)), static_cast<float>(T)) * (1.0f - 0x1p-20f);
     if (parts) {
-      int longest = 0;  // part
+      bool fits = true;  // the longest part
 #pragma unroll 1
       for (int b = b_lo; b < b_hi; ++b) {
         const TreeSeq s = seq(b);
-        if (s.tiles > 0) {
-          const int each = TreeSplit::parts(s.tiles, T, units, p.num_ctas);
-          longest = max(longest, (s.tiles + each - 1) / each);
-        }
+        if (s.tiles > 0) fits = fits && s.tiles <= TreeSplit::parts(s.tiles, spare) * (kUnitTiles + even);
       }
-      parts = __reduce_max_sync(kAll, longest) <= kUnitTiles + TreeSplit::div(all, p.num_ctas);
+      parts = __all_sync(kAll, fits);
     }
     // what is scanned: a sequence's CTAs or its positions, and a unit's
     auto share_of = [&](const TreeSeq &s) {
-      return parts ? TreeSplit::parts(s.tiles, T, units, p.num_ctas) : s.tiles + kUnitTiles;
+      return parts ? TreeSplit::parts(s.tiles, spare) : s.tiles + kUnitTiles;
     };
     sum = 0;
 #pragma unroll 1
@@ -338,8 +336,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       const long long t = __shfl_up_sync(kAll, incl, off);
       if (lane >= off) incl += t;
     }
-    const int W = static_cast<int>(parts ? __shfl_sync(kAll, incl, 31)
-                                         : min(TreeSplit::div(all, kUnitTiles + 1), static_cast<long long>(p.num_ctas)));
+    int W = p.num_ctas;
+    if (parts) W = static_cast<int>(__shfl_sync(kAll, incl, 31));
+    else if (even <= kUnitTiles) W = static_cast<int>(TreeSplit::div(all, kUnitTiles + 1));
     if (static_cast<int>(blockIdx.x) >= W) return;  // the whole CTA
     TreeSplit split = {0, 0, 0, 0};
     long long s0 = blockIdx.x;
@@ -377,8 +376,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     if (parts) {  // part k of the unit
       split.first = static_cast<int>(blockIdx.x) - k;
       split.last = split.first + each - 1;
-      w.tile = static_cast<int>(TreeSplit::div(static_cast<long long>(w.s.tiles) * k, each));
-      w.rem = static_cast<int>(TreeSplit::div(static_cast<long long>(w.s.tiles) * (k + 1), each)) - w.tile;
+      const uint32_t t = w.s.tiles;  // t (k + 1) < 2^32
+      w.tile = static_cast<int>(t * k / each);
+      w.rem = static_cast<int>(t * (k + 1) / each) - w.tile;
     }
     if (tid == 0) *reinterpret_cast<TreeSplit *>(sm + kOffSplit) = split;  // for the merge of cut units
   }
