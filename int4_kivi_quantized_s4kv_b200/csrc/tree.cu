@@ -43,7 +43,7 @@
 // 2800, keys 1850, values 1270, the rest waiting and issuing; 62% of the issue slots) and the chain S, softmax, O, which
 // one set of accumulators leaves no second of.  Measured: 64 sequences of 8192 tokens, 16 nodes, group 4: 394 us, 1.9 TB/s
 // of cache, 0.35 PFLOP/s; 8 of 32768, 64 nodes, group 8: 1400 to 1600 us with the clock, 0.35 to 0.39 PFLOP/s; one of
-// 32768: 44 us; two of 16 tokens: 12.3 us.  For short contexts a unit's beginning and end count for more than its tiles,
+// 32768: 44 us; two of 50 tokens: 11.5 us.  For short contexts a unit's beginning and end count for more than its tiles,
 // and the code that they alone run is fetched each time (5 of 20 warps wait for instructions with 300 tokens a sequence),
 // so that it is kept small: rolled loops, one copy.
 #include <cfloat>
@@ -63,18 +63,19 @@ constexpr int kTreeThreads = 32 * 20;  // 5 warps a scheduler: 96 registers a th
 constexpr int kTile = 128;                 // keys a tile
 constexpr int kTilePages = kTile / kPage;  // 8
 constexpr int kGroupRows = 32;             // query rows of a softmax group
-// Where there are more CTAs than units (TreeSplit).  A part has kMinTiles tiles at least: a tile takes 1 to 2 us, the
-// merge as long as a few.  (1 / 2 / 3 / 4: one sequence of 1000 tokens, 8 kv heads, 18.7 / 20.4 / 20.8 / 24.0 us; four of
-// 500 20.4 / 22.8 / 20.0 / 19.9; one of 300, 2 kv heads, 18.5 / 20.4 / 17.7 / 17.7; from 2000 tokens x 8 on all alike.)
-// A unit has kMaxPieces parts at most, one more for each kTilesAPiece of its tiles: a row's merge reads them all.  (One
-// unit: with 40, 40 + tiles / 16, 40 + tiles / 4 parts 23.0, 21.6, 21.6 us at 16K tokens, 27.0, 25.2, 26.7 at 32K.)
-constexpr int kMinTiles = 3, kMaxPieces = 40, kTilesAPiece = 16;
-// In consecutive ranges, the beginning and end of a unit count as so many tiles.  (3 / 4 / 6 / 8: 128 sequences of 16 to
-// 2000 tokens, 8 kv heads, 202.3 / 196.3 / 191.3 / 181.4 us; 64 of 300 67.7 / 65.7 / 61.3 / 63.0; 24 of 100 to 4000, group
-// 8, 107.7 / 104.6 / 108.0 / 112.7; 64 of 8192 all alike; with 0 a third more on an earlier state.)  Parts leave CTAs
-// without work, ranges give a CTA two units to begin and end: parts are taken while the longest has no more than this
-// many tiles above an even share.  (Parts / ranges: 100 units of 2048, 5120, 10240 tokens 42.7 / 50.0, 75.0 / 71.8,
-// 129.1 / 108.2 us, 2, 9 and 22 tiles above; 76 of them 41.7 / 42.0, 71.5 / 59.3, 128.6 / 90.1, 5, 17 and 36 above.)
+// Where there are more CTAs than units (TreeSplit).  A unit of fewer than kWholeTiles tiles is not cut: the merge costs as
+// much as 4 or 5 tiles, whether its CTAs are two or one a tile.  (Whole below 2 / 6 / 8 tiles, and at least 3 tiles a part:
+// one sequence of 300, 500, 700, 900 tokens, 8 kv heads, 17.4, 18.7, 18.3, 17.7 / 15.8, 17.1, 18.1, 17.7 / 15.7, 17.1, 25.3,
+// 17.7, and 15.7, 17.1, 22.4, 22.2 us.)  It has kMaxPieces parts at most, one more for each kTilesAPiece of its tiles: a
+// row's merge reads them all.  (One unit: with 40, 40 + tiles / 16, 40 + tiles / 4 parts 22.0, 20.7, 20.7 us at 16K tokens,
+// 26.1, 24.4, 26.0 at 32K.)
+constexpr int kWholeTiles = 6, kMaxPieces = 40, kTilesAPiece = 16;
+// In consecutive ranges, the beginning and end of a unit count as so many tiles.  (0 / 3 / 4 / 6 / 8: 128 sequences of 16 to
+// 2000 tokens, 8 kv heads, 242 / 191 / 187 / 188 / 179 us; 64 of 300 71.5 / 67.1 / 65.3 / 60.9 / 63.1; 24 of 100 to 4000,
+// group 8, 141.7 / 107.4 / 105.3 / 109.3 / 112.0; 64 of 8192 all alike.)  Parts leave CTAs without work, ranges give a CTA
+// two units to begin and end: parts are taken while the longest has no more than this many tiles above an even share.
+// (Parts / ranges: 100 units of 2048, 5120, 10240 tokens 39.4 / 47.6, 72.1 / 70.3, 127.3 / 106.8 us, 2, 9 and 22 tiles
+// above; 76 of them 39.6 / 40.8, 69.7 / 57.5, 126.2 / 87.5, 5, 17 and 36 above.)
 constexpr int kUnitTiles = 6;
 constexpr float kRefSlack = 14.0f;         // log2 slack of the softmax reference: weights up to 2^14, finite in fp16
 constexpr float kZeroUnit = 0x1p-10f;      // zero-point shares enter as share * 2^-10 (fp16) against 2^8, in units of 4
@@ -190,7 +191,7 @@ struct TreeSplit {
   // that all units' together are no more than there are
   static __device__ __forceinline__ int parts(int tiles, float spare) {
     const uint32_t t = tiles, c = 1 + static_cast<uint32_t>(static_cast<float>(t) * spare);
-    return max(1u, min(c, min(kMaxPieces + t / kTilesAPiece, t / kMinTiles)));
+    return t < kWholeTiles ? 1 : min(min(c, t), kMaxPieces + t / kTilesAPiece);
   }
 };
 

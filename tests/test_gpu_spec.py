@@ -262,6 +262,8 @@ DEALS = {
     "ranges-one-long": ([(29 * i) % 128 for i in range(70)] + [6300] + [(17 * i) % 128 for i in range(75)],
                         [1 + i % 4 for i in range(146)], 1, 4, 4, 2),
     "ranges-half": ([5500] * 40, [1] * 40, 2, 1, 2, 1),
+    # a part a tile; the shortest units that are cut, and the longest that are not
+    "parts-of-one-tile": ([900, 641, 640, 639], [8, 3, 5, 2], 4, 4, 4, 2),
     # one unit in as many parts as there may be
     "one-unit": ([40000], [5], 1, 4, 4, 2),
     "int8-two-units": ([20011], [7], 2, 7, 8, 2),
