@@ -44,8 +44,8 @@
 // one set of accumulators leaves no second of.  Measured: 64 sequences of 8192 tokens, 16 nodes, group 4: 394 us, 1.9 TB/s
 // of cache, 0.35 PFLOP/s; 8 of 32768, 64 nodes, group 8: 1400 to 1600 us with the clock, 0.35 to 0.39 PFLOP/s; one of
 // 32768: 44 us; two of 50 tokens: 11.5 us.  For short contexts a unit's beginning and end count for more than its tiles,
-// and the code that they alone run is fetched each time (5 of 20 warps wait for instructions with 300 tokens a sequence),
-// so that it is kept small: rolled loops, one copy.
+// and the code that they alone run is fetched each time, so that it is kept small: rolled loops, one copy (64 sequences
+// of 300 tokens: 4 of 20 warps wait for instructions, and 61 us; 6 of 20 and 75 us before).
 #include <cfloat>
 #include <type_traits>
 
