@@ -1,5 +1,5 @@
 // Thin wrappers over the sm_100a fifth-generation tensor-core instructions
-// (tcgen05.*) used by the prefill kernel: tensor-memory allocation, the MMA
+// (tcgen05.*) used by the prefill and tree kernels: tensor-memory allocation, the MMA
 // (A in shared or tensor memory, B in shared memory) and its completion
 // signal on an mbarrier, issued by one elected lane, and the warp-wide
 // tensor-memory loads and stores.

@@ -45,7 +45,7 @@
 // of cache, 0.35 PFLOP/s; 8 of 32768, 64 nodes, group 8: 1400 to 1600 us with the clock, 0.35 to 0.39 PFLOP/s; one of
 // 32768: 44 us; two of 50 tokens: 11.5 us.  For short contexts a unit's beginning and end count for more than its tiles,
 // and the code that they alone run is fetched each time, so that it is kept small: rolled loops, one copy (64 sequences
-// of 300 tokens: 4 of 20 warps wait for instructions, and 61 us; 6 of 20 and 75 us before).
+// of 300 tokens: 57 us, 75 before; of 20 warps 4 waited for instructions at 61 us, 6 at 75).
 #include <cfloat>
 #include <type_traits>
 
@@ -645,8 +645,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
               tc05::tmem_st_frag16(tV + lane_base + (16u << 16) + 8 * pb, o1);
             }
           } else {
-            // two pages a warp, half of a page's tiles at a time
-#pragma unroll 2
+            // two pages a warp, half of a page's tiles at a time (unrolled by 2 64 sequences of 300 tokens took 61.6 us for
+            // 57.3, 64 of 8192 395.4 for 396.2)
+#pragma unroll 1
             for (int ph = 0; ph < 4; ++ph) {
               const int pg = 2 * wq + (ph >> 1), hf = ph & 1;
               if (pg >= np) break;  // the lanes of missing pages hold what they held: their logits are masked
