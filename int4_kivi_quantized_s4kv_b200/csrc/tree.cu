@@ -102,7 +102,7 @@ constexpr uint32_t kOffCut = kOffSplit + 32;                    // [2][2] the cu
 constexpr uint32_t kOffOdd = kOffCut + 4 * 32;                 // [4 pieces][4 V warps] drafted values that are not finite
 constexpr uint32_t kOffSeen = kOffOdd + 64;                     // [2][group][drafted token] the group's rows that see it
 constexpr uint32_t kOffBar = kOffSeen + 2 * 2 * 64 * 4;
-constexpr uint32_t kBars = 36;
+constexpr uint32_t kBars = 38;  // (an even number: the ring behind them is aligned)
 constexpr uint32_t kOffRing = kOffBar + 8 * kBars;
 static_assert(Fmt<4>::kVZero - Fmt<4>::kVScale == 128 && Fmt<2>::kVZero - Fmt<2>::kVScale == 128 &&
                   Fmt<8>::kVZero - Fmt<8>::kVScale == 128, "missing pages: 256 bytes of value scales and zero points");
@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   auto q_free = [&](int x) { return bar(30 + x); };
   auto seen_full = [&](int x) { return bar(32 + x); };
   auto seen_free = [&](int x) { return bar(34 + x); };
+  const uint32_t mma_done = bar(36);  // every product has completed
 
   // ---- barriers and the one-hot operand, while the plan's first loads come
   const int per = (B + 31) >> 5, b_lo = min(B, lane * per), b_hi = min(B, b_lo + per);
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   if (warp == 0) {
     for (int i = lane; i < static_cast<int>(kBars); i += 32) {
       // their arrivals, 4 bits a barrier
-      const unsigned long long counts = i < 16 ? 0x1166AAAAAA111111ull : i < 32 ? 0x1122118818111144ull : 0x8811ull;
+      const unsigned long long counts = i < 16 ? 0x1166AAAAAA111111ull : i < 32 ? 0x1122118818111144ull : 0x118811ull;
       mbar_init(bar(i), static_cast<uint32_t>(counts >> (4 * (i & 15))) & 15u);
     }
     if (lane == 0) *abort_flag = 0;
@@ -844,6 +845,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       w.next(p);
     }
     if (!failed && !issue_pv(kt - 1)) fail();
+    // no product may be under way, nor signal a barrier, once the CTA gives its tensor memory back and leaves: after an
+    // abort nobody else has waited for the last ones
+    if (tc05::elect_one()) tc05::issue_commit(mma_done);
+    __syncwarp();
+    wait_landed(mma_done, 0);
   } else {
     // ------------------------------------------- softmax and the output
     const int g = (warp - kSoftmaxWarp0) >> 2, wq = warp & 3, tl = 32 * wq + lane;
@@ -1168,7 +1174,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       float acc = 0.f;
       for (int y0 = 0; y0 < items; y0 += 64) {
         ok = ok && wait_warp(merged(g), merges & 1);
-        ++merges;
         const int count = ok ? min(64, items - y0) : 0;
 #pragma unroll 4
         for (int y = 0; y < count; ++y) {
@@ -1181,13 +1186,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             ++row;
           }
         }
-        group_sync(bid);  // the items have been read
-        fetch(y0 + 64);
+        if (group_any(bid, !ok)) {
+          // the items on their way must have landed before the CTA leaves, and no more are sent for
+          wait_landed(merged(g), merges & 1);
+          fail();
+          break;
+        }
+        ++merges;
+        fetch(y0 + 64);  // the items have been read
       }
-      if (group_any(bid, !ok)) {
-        fail();
-        break;
-      }
+      if (failed) break;
       group_sync(bid);
       // the last of them leaves the counter at zero
       if (wq == 0 && lane == 0 && (atomicAdd(ticket, 0x10000u) >> 16) + 1 == static_cast<uint32_t>(pieces)) *ticket = 0u;
