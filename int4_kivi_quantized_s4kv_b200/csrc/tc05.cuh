@@ -54,10 +54,17 @@ __host__ __device__ constexpr uint32_t idesc_e5m2_f32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Descriptor of a K-major operand without swizzle, 16 k wide: 8 x 16-byte core
-// matrices (128 bytes), the two along k adjacent (leading-byte offset 128), the
+// Instruction descriptor of a kind::tf32 MMA (fp32 words of which the upper 19
+// bits count), fp32 accumulator, both operands K-major, shape M x N.
+__host__ __device__ constexpr uint32_t idesc_tf32_f32(int M, int N) {
+  return (1u << 4) | (2u << 7) | (2u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Descriptor of a K-major operand without swizzle, 32 bytes of k wide: 8 x 16-byte
+// core matrices (128 bytes), the two along k adjacent (leading-byte offset 128), the
 // next 8 rows behind them (stride 256).
-__device__ __forceinline__ uint64_t smem_desc_plain16(uint32_t addr) {
+__device__ __forceinline__ uint64_t smem_desc_plain32b(uint32_t addr) {
   uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
   d |= static_cast<uint64_t>(128 >> 4) << 16;
   d |= static_cast<uint64_t>(256 >> 4) << 32;
@@ -65,9 +72,16 @@ __device__ __forceinline__ uint64_t smem_desc_plain16(uint32_t addr) {
   return d;
 }
 
-// Byte offset of element (r, k), k < 16, of such an fp16 operand.
-__host__ __device__ __forceinline__ uint32_t plain16_offset(int r, int k) {
-  return static_cast<uint32_t>((r >> 3) * 256 + (k >> 3) * 128 + (r & 7) * 16 + (k & 7) * 2);
+// Byte offset of element (r, k), k < 8, of such a tf32 operand.
+__host__ __device__ __forceinline__ uint32_t plain_tf32_offset(int r, int k) {
+  return static_cast<uint32_t>((r >> 3) * 256 + (k >> 2) * 128 + (r & 7) * 16 + (k & 3) * 4);
+}
+
+// fp32 rounded to tf32 (11 significant bits, fp32's range).
+__device__ __forceinline__ float round_tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return __uint_as_float(r);
 }
 
 // Descriptor of an fp16 operand that lies k-row by k-row (64 columns contiguous,
@@ -159,12 +173,12 @@ __device__ __forceinline__ void issue_f16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// (A in shared memory)
-__device__ __forceinline__ void issue_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// (A in shared memory, K = 8 per MMA)
+__device__ __forceinline__ void issue_tf32_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }

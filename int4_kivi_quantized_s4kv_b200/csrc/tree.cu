@@ -28,8 +28,9 @@
 // against an e5m2 copy of q): the factor 1/4 keeps any fp16 range finite, and a
 // key is carried to about 2^-14 of code * scale, as in prefill attention.  The zero
 // points' share is one number a (page, row): two helper warps compute it with
-// mma.sync (8 pages x 64 rows) and hand it over as an fp16 hi + lo pair, which one
-// more MMA with a constant one-hot operand (token -> page) adds to S.  Values:
+// mma.sync (8 pages x 64 rows) and hand it over as a tf32 hi + lo pair (22 bits and fp32's
+// range: the sum of 128 products of fp16 numbers may be 2^39), which two more MMAs with a
+// constant one-hot operand (token -> page) add to S.  Values:
 // code * scale + zero, rounded once to fp16.  Weights enter as fp16 hi + lo.
 // What is left of the error is the values' rounding, as large as the output's own.
 //
@@ -78,9 +79,9 @@ constexpr int kWholeTiles = 6, kMaxPieces = 40, kTilesAPiece = 16;
 // above; 76 of them 39.6 / 40.8, 69.7 / 57.5, 126.2 / 87.5, 5, 17 and 36 above.)
 constexpr int kUnitTiles = 6;
 constexpr float kRefSlack = 14.0f;         // log2 slack of the softmax reference: weights up to 2^14, finite in fp16
-constexpr float kZeroUnit = 0x1p-10f;      // zero-point shares enter as share * 2^-10 (fp16) against 2^8, in units of 4
 
 constexpr uint32_t kIdescTS = tc05::idesc_f16_f32(128, kTreeRows);
+constexpr uint32_t kIdescTZ = tc05::idesc_tf32_f32(128, kTreeRows);
 constexpr uint32_t kIdescTS8 = tc05::idesc_e5m2_f32(128, kTreeRows);
 constexpr uint32_t kIdescTO = tc05::idesc_f16_f32(128, 2 * kTreeRows) | tc05::kIdescMnB;  // weights hi | lo
 
@@ -92,9 +93,10 @@ constexpr uint32_t kQHiBytes = kTreeRows * 256, kQ8Bytes = kTreeRows * 128, kPBy
 constexpr uint32_t kOffQHi = 0;                              // [2]
 constexpr uint32_t kOffP = kOffQHi + 2 * kQHiBytes;          // [2][hi, lo]
 constexpr uint32_t kOffQ8 = kOffP + 4 * kPBytes;             // [2]
-constexpr uint32_t kOffHot = kOffQ8 + 2 * kQ8Bytes;          // one-hot operand [128][16]
-constexpr uint32_t kOffZero = kOffHot + kTile * 32;          // [2] zero-point operand [64][16]
-constexpr uint32_t kOffRef = kOffZero + 2 * kTreeRows * 32;  // minus the reference, [2][32] fp32
+constexpr uint32_t kOffHot = kOffQ8 + 2 * kQ8Bytes;          // one-hot operand [128][8]
+constexpr uint32_t kZeroBytes = kTreeRows * 32;               // zero-point operand [64][8]
+constexpr uint32_t kOffZero = kOffHot + kTile * 32;          // [2][hi, lo]
+constexpr uint32_t kOffRef = kOffZero + 4 * kZeroBytes;      // minus the reference, [2][32] fp32
 constexpr uint32_t kOffRed = kOffRef + 2 * 32 * 4;           // [2][4][32] fp32
 constexpr uint32_t kOffFlag = kOffRed + 2 * 4 * 32 * 4;      // [2] last-piece flags, tensor memory's address, abort
 constexpr uint32_t kOffSplit = kOffFlag + 16;                  // the TreeSplit
@@ -280,13 +282,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     if (lane == 0) *abort_flag = 0;
     fence_barrier_init();
   }
-  // the one-hot operand: token t counts the shares (hi and lo) of page t / 16, times 2^8
+  // the one-hot operand: token t counts the share of page t / 16, in quarters as the keys
 #pragma unroll 1
   for (int i = tid; i < kTile * 8; i += kTreeThreads) {
-    const int t = i >> 3, k = 2 * (i & 7);
-    uint32_t v = 0;
-    if ((k & 7) == (t / kPage & ~1)) v = (t / kPage & 1) ? 0x5C000000u : 0x00005C00u;
-    sts32(base + kOffHot + tc05::plain16_offset(t, k), v);
+    const int t = i >> 3, k = i & 7;
+    sts32(base + kOffHot + tc05::plain_tf32_offset(t, k), k == t / kPage ? __float_as_uint(0.25f) : 0u);
   }
 
   // ---- plan: every warp finds this CTA's range for itself
@@ -591,18 +591,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
               mma16816(acc[0], a[0], a[1], a[2], a[3], b0, b1);
               mma16816(acc[1], c[0], c[1], c[2], c[3], b0, b1);
             }
-            // shares of pages 2i, 2i + 1 for rows n, n + 8: fp16 hi at k = page, lo at k = 8 + page
-            const uint32_t zo = base + kOffZero + x2 * (kTreeRows * 32);
+            // shares of pages 2i, 2i + 1 for rows n, n + 8, hi and what it leaves
+            const uint32_t zo = base + kOffZero + x2 * (2 * kZeroBytes);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float2 v = make_float2(acc[m][2 * e] * kZeroUnit, acc[m][2 * e + 1] * kZeroUnit);
-                const __half2 hi = __floats2half2_rn(v.x, v.y);
-                const float2 d = sub2(v, __half22float2(hi));
-                const int r = 32 * hw + 16 * m + 8 * e + n;
-                sts32(zo + tc05::plain16_offset(r, 2 * i), h2_as_u32(hi));
-                sts32(zo + tc05::plain16_offset(r, 8 + 2 * i), h2_as_u32(__floats2half2_rn(d.x, d.y)));
+                const float v0 = acc[m][2 * e], v1 = acc[m][2 * e + 1];
+                const float h0 = tc05::round_tf32(v0), h1 = tc05::round_tf32(v1);
+                const uint32_t at = zo + tc05::plain_tf32_offset(32 * hw + 16 * m + 8 * e + n, 2 * i);
+                sts64(at, __float_as_uint(h0), __float_as_uint(h1));
+                sts64(at + kZeroBytes, __float_as_uint(tc05::round_tf32(v0 - h0)), __float_as_uint(tc05::round_tf32(v1 - h1)));
               }
             }
           } else if (is_v) {
@@ -788,7 +787,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     }
   } else if (warp == kMmaWarp) {
     // ------------------- S^T(kt) = K Q^T, then O^T += V^T P^T of tile kt - 1
-    const uint64_t dhot = tc05::smem_desc_plain16(base + kOffHot);
+    const uint64_t dhot = tc05::smem_desc_plain32b(base + kOffHot);
     int kt = 0, uc = 0;
     bool fresh = true;  // tile kt - 1 starts a piece
     auto issue_pv = [&](int k1) {
@@ -828,7 +827,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           if (t > 0) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) tc05::issue_e5m2_ts(tS, tKlo + 8 * j, dq8 + ((32 * j) >> 4), kIdescTS8, 1u);
-            tc05::issue_f16_ss(tS, dhot, tc05::smem_desc_plain16(base + kOffZero + x2 * (kTreeRows * 32)), kIdescTS, 1u);
+            const uint64_t dzero = tc05::smem_desc_plain32b(base + kOffZero + x2 * (2 * kZeroBytes));
+            tc05::issue_tf32_ss(tS, dhot, dzero, kIdescTZ, 1u);
+            tc05::issue_tf32_ss(tS, dhot, dzero + (kZeroBytes >> 4), kIdescTZ, 1u);
           }
           tc05::issue_commit(s_full);
           tc05::issue_commit(k_free(x2));

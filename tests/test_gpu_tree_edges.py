@@ -61,3 +61,19 @@ def test_a_wait_that_runs_out(group_of_rows):
     out = run_tree(c, q, k, v, cu, parents, 16, ws)
     assert c.S.s4kv_get_error(c.gpu) == 0
     assert (np.abs(out - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("key,query,sm_scale,bits", [(1000.0, 128.0, 8e-7, 4), (4096.0, 128.0, 2e-7, 4), (4096.0, 300.0, 8e-8, 8),
+                                                     (12000.0, 50000.0, 1.5e-10, 4), (12000.0, 50000.0, 1.5e-10, 2)])
+def test_zero_points_over_the_whole_range(key, query, sm_scale, bits):
+    """Queries of one sign against zero points of one sign: their product's sum is 128 times the largest of them, far
+    beyond fp16 from finite fp16 inputs, and the answer is finite."""
+    rng = np.random.default_rng(33)
+    c = SpecCache([200, 31, 640], 2, bits, seed=34, key_scale=np.full((2, 128), key))
+    cu, parents, q, k, v = make_tree(rng, [7, 5, 3], 2, 4, 2)
+    q = (query * (1 + 0.02 * q.astype(np.float64))).astype(np.float16)
+    k = (key * k.astype(np.float64)).astype(np.float16)
+    assert np.isfinite(k).all() and all(np.isfinite(x).all() for x in c.k)
+    ref, bound = tree_reference(c, q, k, v, cu, parents, sm_scale)
+    out = run_tree(c, q, k, v, cu, parents, 7, sm_scale=sm_scale)
+    assert (np.abs(out - ref) <= bound).all()
