@@ -35,9 +35,9 @@
 // What is left of the error is the values' rounding, as large as the output's own.
 //
 // Softmax.  Two groups of 4 warps take 32 query rows each; a thread is a token.  The
-// reference of a row is the largest logit of a piece's first tile and moves only when a
-// weight would pass 2^14 (still finite in fp16): a vote of the group decides, and
-// moving it (a maximum over the 128 tokens, the sums and O rescaled) is rare.
+// reference of a row is the largest logit of a piece's first tile in which one is above
+// -infinity, and moves only when a weight would pass 2^14 (still finite in fp16): a vote of the
+// group decides, and moving it (a maximum over the 128 tokens, the sums and O rescaled) is rare.
 //
 // What bounds it: 176 bytes of int4 cache a token feed 512 R operations (R = nodes x G), so that HBM would for few rows
 // and the tensor pipe for many; in fact it is the warps' instruction issue (about 8300 warp instructions a tile: softmax
@@ -871,7 +871,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       float l[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) l[j] = 0.f;
-      float myref = 0.f;  // lane j: the reference of row j (every warp of the group holds the same)
+      float myref = -INFINITY;  // lane j: the reference of row j (every warp of the group holds the same); none yet
+      bool without = true;      // a row of the group has none
       if (rows > 0) {
         if (wq == 0) reinterpret_cast<float *>(sm + kOffRef)[32 * g + lane] = 0.f;
         group_sync(bid);
@@ -935,7 +936,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         auto shift = [&]() { return masked ? shift_as(std::true_type()) : shift_as(std::false_type()); };
         load();
         const float top = shift();
-        if (group_any(bid, top > kRefSlack || t == t0 || !ok)) {
+        if (group_any(bid, top > kRefSlack || without || !ok)) {
           if (group_any(bid, !ok)) {
             fail();
             break;
@@ -944,10 +945,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           red[32 * wq + lane] = warp_reduce_rows(sv, lane, [](float a, float b) { return fmaxf(a, b); });
           group_sync(bid);
           const float up = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));
-          const float by = (t == t0 || up > kRefSlack) ? up : 0.f;
-          const float f = fast_exp2(-by);
-          myref += by;
-          if (wq == 0) reinterpret_cast<float *>(sm + kOffRef)[32 * g + lane] = -myref;
+          const bool none = myref == -INFINITY;  // the sums so far are 0 (or NaN)
+          const float by = none || up > kRefSlack ? up : 0.f;
+          const float f = none ? 1.0f : fast_exp2(-by);
+          myref = none ? by : myref + by;
+          without = __any_sync(kAll, myref == -INFINITY && lane < rows);
+          if (wq == 0) reinterpret_cast<float *>(sm + kOffRef)[32 * g + lane] = myref == -INFINITY ? 0.f : -myref;
           group_sync(bid);
           if (t > t0) {
             // the sums so far, and O once every product before this tile's is in it
@@ -1157,8 +1160,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         float M = -INFINITY, sum = 0.f;
         for (int y = lane; y < pieces; y += 32) {
           const float2 x = __ldcg(p.part_ml + slot_of(y) + lo + r);
-          const float top = fmaxf(M, x.x);
-          sum = sum * fast_exp2(M - top) + x.y * fast_exp2(x.x - top);
+          const float top = fmaxf(M, x.x), at = top == -INFINITY ? 0.f : top;  // (a piece without weight has no reference)
+          sum = sum * fast_exp2(M - at) + x.y * fast_exp2(x.x - at);
           M = top;
           ml[r * pieces + y] = x.x;
         }

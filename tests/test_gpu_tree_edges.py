@@ -3,6 +3,7 @@ are not finite, many rows over a long context."""
 import numpy as np
 import pytest
 
+from int4_kivi_quantized_s4kv_b200 import workloads as W
 from spec_helpers import SpecCache, random_parents, tree_reference
 
 pytestmark = pytest.mark.gpu
@@ -41,6 +42,20 @@ def run_tree(c, q, k, v, cu, parents, max_nodes, ws=None, sm_scale=None):
     return out.float().cpu().numpy().astype(np.float64)
 
 
+def filled(keys, values, bits=4, gpu=True):
+    """A cache of one sequence that holds these keys and values [tokens][heads][128]."""
+    n, heads, _ = keys.shape
+    c = SpecCache([0], heads, bits, room=n // 16 + 1, key_scale=np.ones((heads, 128)), gpu=gpu)
+    c.k, c.v, c.lens = [keys.astype(np.float16)], [values.astype(np.float16)], np.array([n], np.int32)
+    at = W.slot_mapping(c.bt, [np.arange(n)])
+    cu = np.array([0, n], np.int32)
+    assert c.oc.append(c.k[0], c.v[0], at, cu, c.lens, c.bt) == 0
+    if gpu:
+        c.lens_dev = c.dev(c.lens)
+        c.S.s4kv_append(c.gpu, c.dev(c.k[0]), c.dev(c.v[0]), c.dev(at), c.dev(cu), c.lens_dev, c.bt_dev, n)
+    return c
+
+
 @pytest.mark.parametrize("group_of_rows", [0, 1])
 def test_a_wait_that_runs_out(group_of_rows):
     """A counter of pieces that can never reach its count (its low half is about to wrap): the CTAs that share the unit
@@ -77,3 +92,65 @@ def test_zero_points_over_the_whole_range(key, query, sm_scale, bits):
     ref, bound = tree_reference(c, q, k, v, cu, parents, sm_scale)
     out = run_tree(c, q, k, v, cu, parents, 7, sm_scale=sm_scale)
     assert (np.abs(out - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("bad", [float("-inf"), float("nan")])
+@pytest.mark.parametrize("length", [0, 5, 300, 304, 5000])
+def test_keys_that_are_not_finite(bad, length):
+    """A drafted root with -infinity in its key: heads whose query is positive there give it no weight (a softmax over
+    the rest, which for the root of an empty cache is none: NaN), heads whose query is negative have an infinite logit: NaN,
+    in the rows that see it and in no others.  NaN in the key: NaN in all rows that see it."""
+    rng = np.random.default_rng(35)
+    nodes = [13, 9]
+    c = SpecCache([length, 70], 2, seed=36, key_scale=np.ones((2, 128)))
+    cu, parents, q, k, v = make_tree(rng, nodes, 2, 4, 3)
+    parents[6], parents[7] = -1, 6  # a second root, which is the bad one
+    x = 6
+    seen = np.zeros(22, bool)
+    for i in range(13):
+        a = i
+        while a >= 0:
+            seen[i] |= a == x
+            a = parents[a]
+    assert seen[x] and 2 <= seen.sum() < 13
+    q[:, :2, 5], q[:, 2:4, 5] = 8, -8
+    k[x, 0] = 0
+    k[x, 0, 5] = -1100  # as good as -infinity: exp(-774) is 0 in 64 bits
+    ref, bound = tree_reference(c, q, k, v, cu, parents)
+    if length == 0:
+        ref[x, :2] = np.nan
+    ref[seen, 2:4] = np.nan
+    if np.isnan(bad):
+        ref[seen, :4] = np.nan
+    k[x, 0, 5] = bad
+    out = run_tree(c, q, k, v, cu, parents, 13)
+    assert np.array_equal(np.isnan(out), np.isnan(ref))
+    good = ~np.isnan(ref)
+    assert (np.abs(out - ref)[good] <= bound[good]).all()
+    assert c.S.s4kv_get_error(c.gpu) == 0
+
+
+@pytest.mark.parametrize("level", [-2000.0, -120.0, 0.0, 120.0, 2000.0])
+def test_logits_of_one_level_behind_a_key_without_weight(level):
+    """The only key of the first tile has the logit -infinity; all logits behind it are near one level, far below or
+    above 0 (a channel in which all keys are the same, and so exact)."""
+    rng = np.random.default_rng(37)
+    keys, values = rng.standard_normal((112, 1, 128)), rng.standard_normal((112, 1, 128))
+    keys[:, :, 9] = 16
+    c = filled(keys, values)
+    q = rng.standard_normal((1, 1, 128)).astype(np.float16)
+    q[:, :, 9] = level / 16 * 128 ** 0.5
+    ck, cv, up = (x[:, 0] for x in c.cached(0))
+    s = ck @ q[0, 0].astype(np.float64) * 128 ** -0.5
+    w = np.exp(s - s.max())
+    w /= w.sum()
+    # tree_reference's bound over the cached tokens alone, with 2^-14 for the least that a key can lose
+    lost = up * 2.0 ** -13 + 2.0 ** -14 + (2 * np.abs(ck) + up) * 2.0 ** -20
+    d = (lost @ np.abs(q[0, 0].astype(np.float64))).max() * 128 ** -0.5
+    ref = w @ cv
+    bound = 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2 * d + 2.0 ** -19) * (w @ np.abs(cv))
+    k, v = np.zeros((1, 1, 128), np.float16), rng.standard_normal((1, 1, 128)).astype(np.float16)
+    k[0, 0, 5] = -np.inf if q[0, 0, 5] > 0 else np.inf
+    out = run_tree(c, q, k, v, np.array([0, 1], np.int32), np.array([-1], np.int32), 1)[0, 0]
+    assert (np.abs(out - ref) <= bound).all()
+    assert c.S.s4kv_get_error(c.gpu) == 0
