@@ -439,7 +439,9 @@ S4KV_API int s4kv_tree_workspace_size(int num_q_heads, int num_kv_heads, int bat
  *          S4KV_MAX_TREE_NODES.  A sequence with more nodes, or bad cu_nodes
  *          (S4KV_EFLAG_TREE) or a bad length (S4KV_EFLAG_SEQ_LEN), is skipped.
  *  out     device fp16 [n_nodes][num_q_heads][128], 16-B aligned; rows of no
- *          sequence and rows of skipped sequences are left untouched.
+ *          sequence and rows of skipped sequences are left untouched.  It may
+ *          be q itself; else it shares no byte with q, k and v
+ *          (S4KV_ERR_INVALID_ARG).
  *  workspace  device, >= s4kv_tree_workspace_size bytes, 16-B aligned.
  * Any code width of the cache.  Calls sharing one workspace must not overlap
  * on the device. */
@@ -484,7 +486,9 @@ S4KV_API int s4kv_tree_attention(const s4kv_cache_t *cache, const void *q, const
  *          with bad cu_nodes (S4KV_EFLAG_TREE), gets 0 and -1; next_token is -1
  *          too, with S4KV_EFLAG_PROBS, where no target row has a finite
  *          positive sum.
- *  err_flag  device word as in s4kv_cache_t, or NULL. */
+ *  err_flag  device word as in s4kv_cache_t, or NULL.
+ * path, path_len and next_token share no byte with one another, nor with
+ * tokens, parents, cu_nodes and uniforms (S4KV_ERR_INVALID_ARG). */
 S4KV_API int s4kv_verify_tree(const int32_t *tokens, const int32_t *parents,
                               const int32_t *cu_nodes, int n_nodes, int batch,
                               int max_nodes_per_seq, const void *target_probs,
@@ -502,7 +506,9 @@ S4KV_API int s4kv_verify_tree(const int32_t *tokens, const int32_t *parents,
  *  path    device int32 [batch][max_nodes_per_seq]; path_len device int32
  *          [batch]: as s4kv_verify_tree writes them.  0 appends nothing.
  *  seq_lens  device int32 [batch]: lengths BEFORE the append.
- *  new_lens  device int32 [batch], no part of seq_lens: lengths after it.
+ *  new_lens  device int32 [batch]: lengths after it.  It shares no byte with
+ *          seq_lens, path, path_len, cu_nodes and block_tables
+ *          (S4KV_ERR_INVALID_ARG).
  * A sequence with bad cu_nodes or path (S4KV_EFLAG_TREE), or without room in
  * its page table (S4KV_EFLAG_SEQ_LEN), is skipped whole: its new length is its
  * old one. */

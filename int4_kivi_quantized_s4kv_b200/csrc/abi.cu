@@ -52,6 +52,12 @@ int device_shape(DeviceShape *out) {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether two arrays (of n and m 4-byte elements) share a byte.
+bool overlap(const void *p, size_t n, const void *q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return n > 0 && m > 0 && a < b + 4 * m && b < a + 4 * n;
+}
+
 int check_cache(const s4kv_cache_t *c) {
   if (c == nullptr) return S4KV_ERR_INVALID_ARG;
   if (c->head_dim != S4KV_HEAD_DIM || c->page_tokens != S4KV_PAGE_TOKENS) return S4KV_ERR_UNSUPPORTED;
@@ -393,6 +399,12 @@ int s4kv_tree_attention(const s4kv_cache_t *cache, const void *q, const void *k,
       !aligned(parents, 4) || !aligned(seq_lens, 4) || !aligned(block_tables, 4))
     return S4KV_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 16)) return S4KV_ERR_WORKSPACE;
+  // units that are not done yet read these while others write their rows; a query's own row is read before it is written
+  const size_t out_words = static_cast<size_t>(n_nodes) * num_q_heads * (S4KV_HEAD_DIM / 2);
+  const size_t kv_words = static_cast<size_t>(n_nodes) * cache->num_kv_heads * (S4KV_HEAD_DIM / 2);
+  if (overlap(out, out_words, k, kv_words) || overlap(out, out_words, v, kv_words) ||
+      (out != q && overlap(out, out_words, q, out_words)))
+    return S4KV_ERR_INVALID_ARG;
   TreeWs w;
   int ctas = 0;
   rc = tree_ws_layout(num_q_heads, cache->num_kv_heads, batch, max_nodes_per_seq, &w, &ctas);
@@ -451,6 +463,18 @@ int s4kv_verify_tree(const int32_t *tokens, const int32_t *parents, const int32_
       !aligned(path, 4) || !aligned(path_len, 4) || !aligned(next_token, 4) || !aligned(err_flag, 4) ||
       !aligned(target_probs, es) || !aligned(draft_probs, es))
     return S4KV_ERR_INVALID_ARG;
+  // sequences that are not done yet read the inputs while others write their results
+  const size_t seqs = batch, nodes = n_nodes;
+  const struct {
+    const void *p;
+    size_t n;
+  } results[3] = {{path, seqs * max_nodes_per_seq}, {path_len, seqs}, {next_token, seqs}};
+  for (int i = 0; i < 3; ++i) {
+    const auto &r = results[i], &other = results[(i + 1) % 3];
+    if (overlap(r.p, r.n, other.p, other.n) || overlap(r.p, r.n, tokens, nodes) || overlap(r.p, r.n, parents, nodes) ||
+        overlap(r.p, r.n, uniforms, nodes) || overlap(r.p, r.n, cu_nodes, seqs + 1))
+      return S4KV_ERR_INVALID_ARG;
+  }
   VerifyParams p;
   p.tokens = tokens;
   p.parents = parents;
@@ -492,8 +516,12 @@ int s4kv_append_path(const s4kv_cache_t *cache, const void *k, const void *v, in
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_nodes, 4) || !aligned(path, 4) || !aligned(path_len, 4) ||
       !aligned(seq_lens, 4) || !aligned(block_tables, 4) || !aligned(new_lens, 4))
     return S4KV_ERR_INVALID_ARG;
-  // other CTAs of a sequence read its old length while one writes the new one
-  if (new_lens < seq_lens + batch && seq_lens < new_lens + batch) return S4KV_ERR_INVALID_ARG;
+  // other CTAs of a sequence, and other sequences', still read these while one writes its new length
+  const size_t seqs = batch;
+  if (overlap(new_lens, seqs, seq_lens, seqs) || overlap(new_lens, seqs, path_len, seqs) ||
+      overlap(new_lens, seqs, cu_nodes, seqs + 1) || overlap(new_lens, seqs, path, seqs * max_nodes_per_seq) ||
+      overlap(new_lens, seqs, block_tables, seqs * max_pages_per_seq))
+    return S4KV_ERR_INVALID_ARG;
   PathParams p;
   p.pool = static_cast<uint8_t *>(cache->pool);
   p.res_k = static_cast<__half *>(cache->res_k);

@@ -154,3 +154,15 @@ def test_logits_of_one_level_behind_a_key_without_weight(level):
     out = run_tree(c, q, k, v, np.array([0, 1], np.int32), np.array([-1], np.int32), 1)[0, 0]
     assert (np.abs(out - ref) <= bound).all()
     assert c.S.s4kv_get_error(c.gpu) == 0
+
+
+def test_results_in_the_queries_place():
+    """The output may be the queries' own tensor, whole units and cut ones."""
+    rng = np.random.default_rng(39)
+    nodes = [9, 40, 3]
+    c = SpecCache([3000, 100, 7], 2, seed=40, key_scale=np.ones((2, 128)))
+    cu, parents, q, k, v = make_tree(rng, nodes, 2, 4, 3)
+    ref, bound = tree_reference(c, q, k, v, cu, parents)
+    d = [c.dev(x) for x in (q, k, v, cu, parents)]
+    c.S.s4kv_tree_attention(c.gpu, *d, c.lens_dev, c.bt_dev, d[0], 40, c.S.tree_workspace(8, 2, 3, 40))
+    assert (np.abs(d[0].float().cpu().numpy() - ref) <= bound).all()
