@@ -475,7 +475,11 @@ int s4kv_verify_tree(const int32_t *tokens, const int32_t *parents, const int32_
         overlap(r.p, r.n, uniforms, nodes) || overlap(r.p, r.n, cu_nodes, seqs + 1))
       return S4KV_ERR_INVALID_ARG;
   }
+  DeviceShape d;
+  const int rc = device_shape(&d);
+  if (rc != S4KV_OK) return rc;
   VerifyParams p;
+  p.num_sms = d.num_sms;
   p.tokens = tokens;
   p.parents = parents;
   p.cu_nodes = cu_nodes;

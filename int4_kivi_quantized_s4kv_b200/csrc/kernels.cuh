@@ -140,6 +140,7 @@ struct VerifyParams {
   int n_nodes;
   int batch;
   int max_nodes;
+  int num_sms;
 };
 
 // Append of accepted paths (s4kv_append_path).

@@ -37,7 +37,7 @@ namespace {
 constexpr int kThreadsV = 256, kWarpsV = kThreadsV / 32;
 constexpr int kPerLane = 8, kBlockV = 32 * kPerLane;  // entries a warp reads at once
 constexpr int kMaxChunks = 1024;                       // chunk sums a CTA keeps
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 8, kCtasAnSm = 4, kWaveEntries = 9000;
 constexpr unsigned kAllV = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float as_float(float x) { return x; }
@@ -73,7 +73,7 @@ __device__ __forceinline__ double warp_sum(double x) {
 
 // blocks: groups of kBlockV entries in a chunk (1 but for vocabularies in the millions).
 template <typename T>
-__global__ void __launch_bounds__(kThreadsV, 4) verify_kernel(const VerifyParams p, int blocks) {
+__global__ void __launch_bounds__(kThreadsV, kCtasAnSm) verify_kernel(const VerifyParams p, int blocks) {
   __shared__ int tok[S4KV_MAX_TREE_NODES], out_path[S4KV_MAX_TREE_NODES];
   __shared__ double at_p[S4KV_MAX_TREE_NODES], at_q[S4KV_MAX_TREE_NODES], at_u[S4KV_MAX_TREE_NODES];
   __shared__ double chunk_sum[kMaxChunks];
@@ -294,10 +294,25 @@ __global__ void __launch_bounds__(kThreadsV, 4) verify_kernel(const VerifyParams
 
 template <typename T>
 static cudaError_t launch_verify_for(const VerifyParams &p, cudaStream_t stream) {
-  // CTAs a sequence: as many as share its row's reading while the sequences alone do not fill the card
-  // (148 SMs of 8 CTAs), and no more than there are chunks
-  int cluster = kMaxCluster;
-  while (cluster > 1 && (p.batch >= 2 * 148 * 8 / cluster || p.vocab <= kBlockV * (cluster / 2))) cluster /= 2;
+  // CTAs a sequence: the number that takes the shortest time, as waves of what is on the card at once, each of a fixed
+  // part (walk, exchange, draw) as long as kWaveEntries entries and a CTA's share of the row.  Of 4 CTAs an SM clusters
+  // of 4 and 8 leave one in 25 idle (148 SMs: 71 clusters of 8, 142 of 4, 296 of 2, by the occupancy query); no more
+  // CTAs than leave each warp a chunk of its own.  Measured, fp32 with draft rows, us for 8 / 4 / 2 / 1:
+  //   128256 entries: 70 sequences 16 / 21 / 34 / -, 74 22.5 / 22.3 / 35 / 61, 136 31 / 26 / 40 / -, 200 44 / 45 / 43 / 71,
+  //   296 66 / 61 / 47 / 72, 400 83 / 70 / 77 / 77, 592 119 / 105 / 89 / 85, 800 158 / 131 / 120 / 140, 1600 - / - / 224 / 217
+  //   32000: 70 8.4 / 8.5 / 10.7 / -, 74 12.6 / 8.7 / 10.7 / 15.3, 136 15 / 10.3 / 11.3 / -, 144 18 / 13.9 / 11.5 / -,
+  //   296 36 / 26 / 16 / 21, 400 46 / 31 / 29 / 25, 800 89 / 58 / 44 / 46, 1600 - / - / 81 / 69
+  //   4000: 70 7.5 / 6.5 / 6.5 / 6.6
+  int cluster = 1;
+  long long best = 0;
+  for (int c = 1; c <= kMaxCluster && (c == 1 || p.vocab > kBlockV * kWarpsV * (c / 2)); c *= 2) {
+    const int slots = kCtasAnSm * p.num_sms, at_once = (c > 2 ? slots - slots / 25 : slots) / c;
+    const long long t = static_cast<long long>((p.batch - 1) / at_once + 1) * (p.vocab / c + kWaveEntries);
+    if (c == 1 || t < best) {
+      best = t;
+      cluster = c;
+    }
+  }
   const int blocks = static_cast<int>((static_cast<long long>(p.vocab) / cluster + 1) / (static_cast<long long>(kBlockV) * (kMaxChunks - 2)) + 1);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
