@@ -444,7 +444,16 @@ S4KV_API int s4kv_tree_workspace_size(int num_q_heads, int num_kv_heads, int bat
  *          (S4KV_ERR_INVALID_ARG).
  *  workspace  device, >= s4kv_tree_workspace_size bytes, 16-B aligned.
  * Any code width of the cache.  Calls sharing one workspace must not overlap
- * on the device. */
+ * on the device.
+ * Accuracy: the part code * scale of a quantized key enters to 2^-13 of
+ * itself where it is above 1, else to 2^-14, or to 2^-11 of itself where that
+ * is less; zero points and sums in fp32 (zero points to 2^-22); a
+ * dequantized value rounded to fp16 (one beyond 65504, which inputs within
+ * 2^-11 of that can give, is infinite); weights to 2^-20; the output rounded
+ * to fp16.
+ * A drafted key or value that is not finite reaches the rows that see it and
+ * no others; a logit of -infinity is a weight of 0, and a row of nothing
+ * else is NaN. */
 S4KV_API int s4kv_tree_attention(const s4kv_cache_t *cache, const void *q, const void *k,
                                  const void *v, int num_q_heads, int n_nodes,
                                  const int32_t *cu_nodes, const int32_t *parents,

@@ -25,8 +25,10 @@
 // straight-line code as in decode attention and no dequantized byte goes through
 // shared memory.  Keys: S = sum q (code scale) + sum q zero.  code/4 * scale is kept as
 // its fp16 rounding and the exact remainder, cut to e5m2 (a second, fp8 MMA
-// against an e5m2 copy of q): the factor 1/4 keeps any fp16 range finite, and a
-// key is carried to about 2^-14 of code * scale, as in prefill attention.  The zero
+// against an e5m2 copy of q): the factor 1/4 keeps any fp16 range finite.  Of a product
+// code * scale above 1 the cut loses less than 2^-14, and q's rounding 2^-3 of the remainder, at
+// most 2^-14 more; below 1 the cut loses less than 2^-14 itself (e5m2's smallest step 2^-16, times 4),
+// and below 1/8 there is no remainder left: the product is its fp16 rounding (2^-11 of it).  The zero
 // points' share is one number a (page, row): two helper warps compute it with
 // mma.sync (8 pages x 64 rows) and hand it over as a tf32 hi + lo pair (22 bits and fp32's
 // range: the sum of 128 products of fp16 numbers may be 2^39), which two more MMAs with a
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
                   const uint32_t c4 = hmul2_u32(a[r], quarter_unit<kBits>()), sr = s[2 * q + (r >> 1)];
                   const uint32_t hr = hmul2_u32(c4, sr);
                   hi[4 * q + r] = hr;
-                  rem[r] = h2_as_u32(__hfma2(u32_as_h2(c4), u32_as_h2(sr), __hneg2(u32_as_h2(hr))));  // exact
+                  rem[r] = h2_as_u32(__hfma2(u32_as_h2(c4), u32_as_h2(sr), __hneg2(u32_as_h2(hr))));  // exact (above fp16's smallest step)
                 }
                 // an fp16 number's upper byte is its e5m2 truncation (3 significant bits of the remainder)
                 lo[2 * q] = __byte_perm(rem[0], rem[2], 0x7531);

@@ -3,8 +3,8 @@ are not finite, many rows over a long context."""
 import numpy as np
 import pytest
 
-from int4_kivi_quantized_s4kv_b200 import workloads as W
 from spec_helpers import SpecCache, random_parents, tree_reference
+from tree_helpers import REMAINDER_BOUND, ROWS, SM_SCALE, TOKENS, filled, remainder_case, remainder_error
 
 pytestmark = pytest.mark.gpu
 
@@ -40,20 +40,6 @@ def run_tree(c, q, k, v, cu, parents, max_nodes, ws=None, sm_scale=None):
                             ws, sm_scale)
     torch.cuda.synchronize()
     return out.float().cpu().numpy().astype(np.float64)
-
-
-def filled(keys, values, bits=4, gpu=True):
-    """A cache of one sequence that holds these keys and values [tokens][heads][128]."""
-    n, heads, _ = keys.shape
-    c = SpecCache([0], heads, bits, room=n // 16 + 1, key_scale=np.ones((heads, 128)), gpu=gpu)
-    c.k, c.v, c.lens = [keys.astype(np.float16)], [values.astype(np.float16)], np.array([n], np.int32)
-    at = W.slot_mapping(c.bt, [np.arange(n)])
-    cu = np.array([0, n], np.int32)
-    assert c.oc.append(c.k[0], c.v[0], at, cu, c.lens, c.bt) == 0
-    if gpu:
-        c.lens_dev = c.dev(c.lens)
-        c.S.s4kv_append(c.gpu, c.dev(c.k[0]), c.dev(c.v[0]), c.dev(at), c.dev(cu), c.lens_dev, c.bt_dev, n)
-    return c
 
 
 @pytest.mark.parametrize("group_of_rows", [0, 1])
@@ -166,3 +152,28 @@ def test_results_in_the_queries_place():
     d = [c.dev(x) for x in (q, k, v, cu, parents)]
     c.S.s4kv_tree_attention(c.gpu, *d, c.lens_dev, c.bt_dev, d[0], 40, c.S.tree_workspace(8, 2, 3, 40))
     assert (np.abs(d[0].float().cpu().numpy() - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("bits", [4, 8, 2])
+def test_remainders_of_the_keys(bits):
+    """What fp16 loses of code * scale comes back through the second product: measured alone, where the logits without
+    it would be off by 1 of this measure, and by 2 with it subtracted."""
+    c, q, exact, parts, _ = remainder_case(bits, True)
+    k, v = np.zeros((ROWS, 1, 128), np.float16), np.zeros((ROWS, 1, 128), np.float16)
+    v[:, 0, 127] = 1
+    level = (2 ** bits - 1) / 2 ** bits
+    out = run_tree(c, q, k, v, np.array([0, ROWS], np.int32), np.full(ROWS, -1, np.int32), ROWS, sm_scale=SM_SCALE)[:, 0]
+    logits = np.log(out[:, :TOKENS] / level) - np.log(out[:, 127:])
+    assert remainder_error(logits, exact, parts) <= REMAINDER_BOUND
+
+
+def test_many_rows_over_a_long_context():
+    """512 query rows a kv head over 6011 tokens, 8 blocks of rows, and 448 over 2100."""
+    rng = np.random.default_rng(41)
+    nodes = [64, 56]
+    c = SpecCache([6011, 2100], 2, seed=42, key_scale=np.ones((2, 128)))
+    cu, parents, q, k, v = make_tree(rng, nodes, 2, 8, 4)
+    ref, bound = tree_reference(c, q, k, v, cu, parents)
+    out = run_tree(c, q, k, v, cu, parents, 64)
+    assert (np.abs(out - ref) <= bound).all()
+    assert c.S.s4kv_get_error(c.gpu) == 0

@@ -4,6 +4,8 @@ import ctypes
 
 import pytest
 
+from tree_helpers import REMAINDER_BOUND, remainder_case, remainder_error
+
 
 @pytest.fixture(scope="module")
 def S():
@@ -67,3 +69,45 @@ def test_append_path_refuses_new_lengths_in_its_inputs(S):
             got = S.lib().s4kv_append_path(ctypes.byref(c), P(a["k"]), P(a["v"]), 12, P(a["cu"]), P(a["path"]), P(a["ln"]), 3,
                                            P(a["sl"]), P(a["bt"]), 4, 2, P(a[x] + at), P(0))
             assert got == S.ERR_INVALID_ARG, (x, at)
+
+
+@pytest.mark.parametrize("bits", [4, 8, 2])
+def test_the_measure_of_the_keys_remainders_tells_them_from_none(oracle_mod, bits):
+    """The kernel's arithmetic passes; without the remainders, with half, twice or minus them it does not."""
+    _, _, exact, parts, emulation = remainder_case(bits, False)
+    assert remainder_error(emulation(1), exact, parts) <= REMAINDER_BOUND
+    for wrong in (0, 0.5, 2, -1):
+        assert remainder_error(emulation(wrong), exact, parts) > REMAINDER_BOUND, wrong
+
+
+class Elsewhere:
+    """A tensor's type, shape and address on a device that this machine need not have."""
+
+    def __init__(self, t, device):
+        self.t, self.device, self.dtype, self.shape = t, device, t.dtype, t.shape
+
+    def get_device(self):
+        return self.device
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("moved", range(8))
+def test_wrappers_refuse_tensors_on_two_devices(S, moved):
+    import torch
+    i32 = lambda *x: torch.zeros(*x, dtype=torch.int32)  # noqa: E731
+    f16 = lambda *x: torch.zeros(*x, dtype=torch.float16)  # noqa: E731
+    cache = S.S4KVCache(4, 1, 1, device="cpu")
+    cache.pool = Elsewhere(cache.pool, 0)
+    at = lambda ts: [Elsewhere(t, 1 if i == moved else 0) for i, t in enumerate(ts)]  # noqa: E731
+    q, k, v, cu, par, sl, bt, out = at([f16(2, 4, 128), f16(2, 1, 128), f16(2, 1, 128), i32(2), i32(2), i32(1), i32(1, 3), f16(2, 4, 128)])
+    with pytest.raises(ValueError, match="all tensors must be on CUDA device 0"):
+        S.s4kv_tree_attention(cache, q, k, v, cu, par, sl, bt, out, 2, Elsewhere(torch.zeros(16, dtype=torch.uint8), 0))
+    k, v, cu, path, ln, sl, bt, new = at([f16(2, 1, 128), f16(2, 1, 128), i32(2), i32(1, 2), i32(1), i32(1), i32(1, 3), i32(1)])
+    with pytest.raises(ValueError, match="all tensors must be on CUDA device 0"):
+        S.s4kv_append_path(cache, k, v, cu, path, ln, sl, bt, new)
+    if moved:  # the first one names the device
+        t, tok, par, cu, q, u, path, ln = at([torch.zeros(2, 5), i32(2), i32(2), i32(2), torch.zeros(2, 5), torch.zeros(2), i32(1, 2), i32(1)])
+        with pytest.raises(ValueError, match="all tensors must be on CUDA device 0"):
+            S.s4kv_verify_tree(tok, par, cu, t, q, u, path, ln, Elsewhere(i32(1), 0))
