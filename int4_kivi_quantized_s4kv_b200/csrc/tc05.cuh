@@ -77,12 +77,8 @@ __host__ __device__ __forceinline__ uint32_t plain_tf32_offset(int r, int k) {
   return static_cast<uint32_t>((r >> 3) * 256 + (k >> 2) * 128 + (r & 7) * 16 + (k & 3) * 4);
 }
 
-// fp32 rounded to tf32 (11 significant bits, fp32's range).
-__device__ __forceinline__ float round_tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return __uint_as_float(r);
-}
+// fp32 rounded to tf32 (11 significant bits, fp32's range), half a step away from zero; a NaN may become a number.
+__device__ __forceinline__ float round_tf32(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xFFFFE000u); }
 
 // Descriptor of an fp16 operand that lies k-row by k-row (64 columns contiguous,
 // "MN-major") with the 128-byte swizzle: 8 rows of 64 columns make an atom of 1024
