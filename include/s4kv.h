@@ -446,7 +446,7 @@ S4KV_API int s4kv_tree_workspace_size(int num_q_heads, int num_kv_heads, int bat
  * Any code width of the cache.  Calls sharing one workspace must not overlap
  * on the device.
  * Accuracy: the part code * scale of a quantized key enters to 2^-13 of
- * itself where it is above 1, else to 2^-14, or to 2^-11 of itself where that
+ * itself where it is above 1, else to 2^-13, or to 2^-11 of itself where that
  * is less; zero points and sums in fp32 (zero points to 2^-21); a
  * dequantized value rounded to fp16 (one beyond 65504, which inputs within
  * 2^-11 of that can give, is infinite); weights to 2^-20; the output rounded

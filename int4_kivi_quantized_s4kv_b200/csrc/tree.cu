@@ -42,13 +42,13 @@
 // group decides, and moving it (a maximum over the 128 tokens, the sums and O rescaled) is rare.
 //
 // What bounds it: 176 bytes of int4 cache a token feed 512 R operations (R = nodes x G), so that HBM would for few rows
-// and the tensor pipe for many; in fact it is the warps' instruction issue (about 8300 warp instructions a tile: softmax
-// 2800, keys 1850, values 1270, the rest waiting and issuing; 62% of the issue slots) and the chain S, softmax, O, which
-// one set of accumulators leaves no second of.  Measured: 64 sequences of 8192 tokens, 16 nodes, group 4: 394 us, 1.9 TB/s
-// of cache, 0.35 PFLOP/s; 8 of 32768, 64 nodes, group 8: 1400 to 1600 us with the clock, 0.35 to 0.39 PFLOP/s; one of
-// 32768: 44 us; two of 50 tokens: 11.5 us.  For short contexts a unit's beginning and end count for more than its tiles,
+// and the tensor pipe for many; in fact it is the warps' instruction issue (8100 to 8600 warp instructions a tile, of them
+// softmax 2800, keys 1850, values 1270, the rest waiting and issuing; 60 to 69% of the issue slots) and the chain S, softmax,
+// O, which one set of accumulators leaves no second of.  Measured, captured and warm: 64 sequences of 8192 tokens, 16 nodes,
+// group 4: 402 us, 1.9 TB/s of cache, 0.34 PFLOP/s; 8 of 32768, 64 nodes, group 8: 1480 to 1590 us with the clock, 0.35 to
+// 0.37 PFLOP/s; one of 32768: 43 us; two of 50 tokens: 11.4 us.  For short contexts a unit's beginning and end count for more than its tiles,
 // and the code that they alone run is fetched each time, so that it is kept small: rolled loops, one copy (64 sequences
-// of 300 tokens: 57 us, 75 before; of 20 warps 4 waited for instructions at 61 us, 6 at 75).
+// of 300 tokens: 59 us, 75 with loops unrolled; of 20 warps 4 waited for instructions at 61 us, 6 at 75).
 #include <cfloat>
 #include <type_traits>
 

@@ -20,9 +20,9 @@
 // clusters of 8 is on the card at once (128 registers: two waves).
 // Bound by HBM for many sequences (one target row each, and one draft row after a
 // rejection), by the chain of a row's sum and its exchange for few.  Measured, captured
-// and warm: 64 chains of 8 over 128256 fp32 entries with draft rows 19.6 us (27 with an
-// empty L2: 2.4 TB/s), 48 trees over bf16 rows without 13.8, 16 trees of 12 over 32000
-// fp16 entries with draft rows 10.7, one chain of 5 over 32000 6.8.
+// and warm: 64 chains of 8 over 128256 fp32 entries with draft rows 19.5 us (21.4 a call
+// with an empty L2: 3.1 TB/s), 48 trees over bf16 rows without 14.0, 16 trees of 12 over 32000
+// fp16 entries with draft rows 10.6, one chain of 5 over 32000 6.5.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
