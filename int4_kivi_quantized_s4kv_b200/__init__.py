@@ -402,7 +402,8 @@ def s4kv_tree_attention(cache: S4KVCache, q, k, v, cu_nodes, parents, seq_lens, 
     keys and values k, v fp16 [n_nodes][kv_heads][128], not in the cache) over
     the cached tokens, their ancestors in the tree and themselves.  Sequence b
     owns the nodes cu_nodes[b] .. cu_nodes[b+1]-1; parents int32 [n_nodes] are
-    indices inside the sequence, -1 for a child of the last cached token."""
+    indices inside the sequence, -1 for a child of the last cached token.  out
+    may be q itself, else a tensor of its own."""
     import torch
     n_nodes, num_q_heads = q.shape[0], q.shape[1]
     batch, max_pages = block_tables.shape
@@ -425,7 +426,8 @@ def s4kv_verify_tree(tokens, parents, cu_nodes, target_probs, draft_probs, unifo
     what follows node i; rows may be strided), with uniforms fp32 [n_nodes] in
     [0, 1).  draft_probs: the rows from which each node's children were drawn,
     or None for proposals chosen without randomness.  Fills path int32
-    [batch][max_nodes], path_len and next_token int32 [batch]."""
+    [batch][max_nodes], path_len and next_token int32 [batch], tensors of
+    their own."""
     import torch
     n_nodes, vocab = target_probs.shape
     batch, max_nodes = path.shape
